@@ -75,6 +75,7 @@ extern "C" {
 #define PA_ERR_ALIGN        (-8)  /* a device pointer is not 16-byte aligned */
 #define PA_ERR_DEVICE       (-9)  /* no usable sm_103 device / kernel image */
 #define PA_ERR_TIMEOUT      (-10) /* a kernel gave up on a stuck asynchronous copy */
+#define PA_ERR_NO_BLOCKS    (-11) /* the free ring holds too few blocks for the step */
 
 /* ---- dtype codes -------------------------------------------------------- */
 #define PA_F32  0
@@ -131,6 +132,141 @@ PA_API int pa_reshape_and_cache(const void* k, const void* v, int64_t num_tokens
                          const int64_t* slot_mapping, void* key_cache,
                          void* value_cache, int64_t num_blocks,
                          int block_size, void* stream);
+
+/*
+ * Step bookkeeping on the GPU: block tables, positions and slot maps from
+ * request lengths, with the free blocks in device memory, so a step can be
+ * planned without a host round trip and captured in a CUDA graph. The rules
+ * are the host pool's ([P1] §3.2 BlockPool: a request takes blocks from the
+ * head of the free list only when its last block is full, freed blocks go to
+ * the tail) for blocks that one request owns; blocks shared copy-on-write
+ * stay with the host pool.
+ *
+ * Free ring: free_ring int32 [ring_size] and ring_state int64 [2] = {head,
+ * tail}, running counters with 0 <= head <= tail <= head + ring_size. Entry
+ * i of the list sits at free_ring[i % ring_size]; entries head .. tail - 1
+ * are free, in the order in which they will be handed out.
+ *
+ * pa_extend_block_tables — request r holds context_lens[r] tokens, whose
+ * blocks are in its table row, and gets new_tokens[r] more. In request
+ * order, each request appends the blocks it lacks from the head of the ring.
+ *   query_start_loc  int32 [num_seqs + 1], written: first token row of each
+ *                    request, and the total.
+ *   block_start_loc  int32 [num_seqs + 1], written: the same for the blocks
+ *                    handed out by this call.
+ *   seq_lens         int32 [num_seqs], written: context plus new tokens; may
+ *                    be context_lens.
+ *   positions, slot_mapping  int64 [num_tokens], written: position and pool
+ *                    slot of each new token, as pa_compute_slot_mapping gives
+ *                    them. num_tokens is the number of rows on the host side
+ *                    (an upper bound): rows behind the last token get
+ *                    position 0 and slot -1 (PAD).
+ *   block_tables     int32 [num_seqs][block_tables_stride]: entries of the
+ *                    new blocks are written, no others.
+ *   ring_state_out   int64 [2], written: the state after the call; may be
+ *                    ring_state.
+ * The step is taken whole or not at all: if the ring holds too few blocks
+ * (latches PA_ERR_NO_BLOCKS), or the new tokens exceed num_tokens or the
+ * ring state is inconsistent (PA_ERR_OUT_OF_RANGE), every request gets no
+ * token, the state and the tables stay as they are and seq_lens =
+ * context_lens. A request with a negative length, or whose total exceeds
+ * its table row, gets no token and latches PA_ERR_OUT_OF_RANGE; the others
+ * are served. Blocks outside the pool (in the ring or the table) give slot
+ * -1 and latch PA_ERR_OUT_OF_RANGE.
+ *
+ * pa_release_block_tables — the blocks of requests with finished[r] != 0 go
+ * to the tail of the ring: row by row, the entries of the first
+ * ceil(seq_lens[r] / block_size) table columns, in order. Negative entries
+ * (blocks released before, e.g. by a sliding window) are passed over;
+ * entries >= num_blocks are passed over and latch PA_ERR_OUT_OF_RANGE.
+ *   finished          uint8 [num_seqs], device.
+ *   release_start_loc int32 [num_seqs + 1], written: where each request's
+ *                     blocks begin among those returned, and their number.
+ *   seq_lens_out      int32 [num_seqs], written: 0 for released requests,
+ *                     seq_lens otherwise; may be seq_lens. The table rows
+ *                     are left as they are: keep the length of 0 with them,
+ *                     or the same blocks would be returned twice.
+ * A release that the ring has no room for, or an inconsistent ring state,
+ * latches PA_ERR_OUT_OF_RANGE and changes nothing. A finished request whose
+ * length is negative or exceeds its table row is left alone (same code).
+ * One block held by two requests is a caller error.
+ *
+ * Both are asynchronous and need no workspace. block_size >= 1,
+ * num_tokens and ring_size below 2^31. int32 pointers must be 4-byte and
+ * int64 pointers 8-byte aligned.
+ */
+PA_API int pa_extend_block_tables(const int32_t* context_lens, const int32_t* new_tokens,
+                                  int num_seqs, int32_t* block_tables,
+                                  int64_t block_tables_stride, int block_size,
+                                  int64_t num_blocks, const int32_t* free_ring,
+                                  int64_t ring_size, const int64_t* ring_state,
+                                  int64_t* ring_state_out, int64_t num_tokens,
+                                  int32_t* query_start_loc, int32_t* block_start_loc,
+                                  int32_t* seq_lens, int64_t* positions,
+                                  int64_t* slot_mapping, void* stream);
+PA_API int pa_release_block_tables(const uint8_t* finished, const int32_t* seq_lens, int num_seqs,
+                                   const int32_t* block_tables, int64_t block_tables_stride,
+                                   int block_size, int64_t num_blocks, int32_t* free_ring,
+                                   int64_t ring_size, const int64_t* ring_state,
+                                   int64_t* ring_state_out, int32_t* release_start_loc,
+                                   int32_t* seq_lens_out, void* stream);
+
+/*
+ * pa_rotary_reshape_and_cache — rotary positions of q and k fused with the
+ * KV write: pair i of a head's first rot_size dims is turned by
+ *     angle = positions[axis_of_pair[i]][t] * inv_freq[i]
+ *     (a, b) -> (a cos(angle) - b sin(angle), b cos(angle) + a sin(angle))
+ * with (a, b) = (x[i], x[i + rot_size/2]), or (x[2i], x[2i + 1]) when
+ * interleaved != 0; dims rot_size .. head_size - 1 pass. Several axes serve
+ * image and video tokens (time, height, width). Arithmetic is fp32 on angles
+ * reduced exactly to one turn (any int64 position with |position * inv_freq|
+ * meaningful in fp64); results are rounded once to the stored type.
+ *   q            num_tokens rows of [num_q_heads][head_size], q_stride
+ *                elements apart; k, v likewise with num_kv_heads: slices of
+ *                one fused projection need no copy.
+ *   q_out        rows of [num_q_heads][head_size], q_out_stride elements
+ *                apart; every row is written. May be q with the same stride.
+ *   positions    int64 [num_axes], rows of num_tokens, position_stride apart.
+ *   inv_freq     float64 [rot_size / 2], device.
+ *   axis_of_pair int32 [rot_size / 2], device, entries in [0, num_axes)
+ *                (others latch PA_ERR_OUT_OF_RANGE and count as 0); NULL:
+ *                axis 0 for every pair.
+ * The rotated k and v are written as by pa_reshape_and_cache (same slots,
+ * PAD and errors); pools have q's dtype. head_size and rot_size are
+ * multiples of 16, rot_size <= head_size <= 256, 1 <= num_axes <= 8; strides
+ * are multiples of 16 bytes and at least one row (PA_ERR_SHAPE /
+ * PA_ERR_ALIGN).
+ *
+ * pa_rotary_reshape_and_cache_fp8 — into E4M3 pools with one scale per pool,
+ * code = e4m3(rotated / scale): the fp32 value is quantised, without a
+ * rounding to the 16-bit type in between.
+ * pa_rotary_reshape_and_cache_fp8_scaled — into E4M3 blocks that carry their
+ * own scales, fixed as by pa_reshape_and_cache_fp8_scaled from the rotated
+ * values.
+ */
+PA_API int pa_rotary_reshape_and_cache(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+    int dtype, const int64_t* positions, int64_t position_stride, int num_axes,
+    const double* inv_freq, const int32_t* axis_of_pair, int rot_size, int interleaved,
+    const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* key_cache,
+    void* value_cache, int64_t num_blocks, int block_size, void* stream);
+PA_API int pa_rotary_reshape_and_cache_fp8(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+    int dtype, const int64_t* positions, int64_t position_stride, int num_axes,
+    const double* inv_freq, const int32_t* axis_of_pair, int rot_size, int interleaved,
+    const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* key_cache,
+    void* value_cache, int64_t num_blocks, int block_size, float k_scale, float v_scale,
+    void* stream);
+PA_API int pa_rotary_reshape_and_cache_fp8_scaled(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+    int dtype, const int64_t* positions, int64_t position_stride, int num_axes,
+    const double* inv_freq, const int32_t* axis_of_pair, int rot_size, int interleaved,
+    const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* key_cache,
+    void* value_cache, int64_t num_blocks, int block_size, float* k_scales, float* v_scales,
+    void* stream);
 
 /*
  * Scratch needed by pa_decode_attention for the same arguments

@@ -20,6 +20,7 @@ STATUS_NAMES = {
     0: "PA_OK", -1: "PA_ERR_NULL", -2: "PA_ERR_SHAPE", -3: "PA_ERR_DTYPE",
     -4: "PA_ERR_WORKSPACE", -5: "PA_ERR_OUT_OF_RANGE", -6: "PA_ERR_CUDA",
     -7: "PA_ERR_ALIAS", -8: "PA_ERR_ALIGN", -9: "PA_ERR_DEVICE", -10: "PA_ERR_TIMEOUT",
+    -11: "PA_ERR_NO_BLOCKS",
 }
 DTYPE_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -71,6 +72,19 @@ SIGNATURES = {
     "pa_map_to_kernel_blocks": ([_c_p, _c_i64, _c_i64, _c_i64, _c_i32, _c_p, _c_i64, _c_p],
                                 _c_i32),
 }
+
+_ROTARY = ([_c_p, _c_i64] * 3 + [_c_i64] + [_c_i32] * 4 + [_c_p, _c_i64, _c_i32, _c_p, _c_p,
+                                                           _c_i32, _c_i32, _c_p, _c_p, _c_i64,
+                                                           _c_p, _c_p, _c_i64, _c_i32])
+SIGNATURES.update({
+    "pa_extend_block_tables": ([_c_p, _c_p, _c_i32, _c_p, _c_i64, _c_i32, _c_i64, _c_p, _c_i64,
+                                _c_p, _c_p, _c_i64] + [_c_p] * 6, _c_i32),
+    "pa_release_block_tables": ([_c_p, _c_p, _c_i32, _c_p, _c_i64, _c_i32, _c_i64, _c_p, _c_i64]
+                                + [_c_p] * 5, _c_i32),
+    "pa_rotary_reshape_and_cache": (_ROTARY + [_c_p], _c_i32),
+    "pa_rotary_reshape_and_cache_fp8": (_ROTARY + [_c_f, _c_f, _c_p], _c_i32),
+    "pa_rotary_reshape_and_cache_fp8_scaled": (_ROTARY + [_c_p, _c_p, _c_p], _c_i32),
+})
 
 _lock = threading.Lock()
 _lib = None

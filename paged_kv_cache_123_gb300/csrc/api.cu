@@ -44,6 +44,9 @@ int device_setup(int* dev_out) {
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned(const void* p, uintptr_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
 inline bool pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
 
 int elt_bytes(int dtype) {
@@ -54,6 +57,8 @@ int elt_bytes(int dtype) {
   }
   return 0;
 }
+
+int run_rotary(pa::RotaryArgs& a, void* stream);
 
 int check_launch(cudaError_t e) {
   if (e == cudaSuccess) return PA_OK;
@@ -262,6 +267,7 @@ const char* pa_status_string(int status) {
     case PA_ERR_ALIGN: return "device pointer not 16-byte aligned";
     case PA_ERR_DEVICE: return "no usable sm_103 device or kernel image";
     case PA_ERR_TIMEOUT: return "a kernel gave up waiting on an asynchronous copy";
+    case PA_ERR_NO_BLOCKS: return "the free ring holds too few blocks";
   }
   return "unknown status";
 }
@@ -723,6 +729,113 @@ int pa_map_to_kernel_blocks(const int32_t* manager_table, int64_t num_rows,
       kernel_stride, g_sm_count[dev], (cudaStream_t)stream, g_err_ptr[dev]));
 }
 
+int pa_extend_block_tables(const int32_t* context_lens, const int32_t* new_tokens, int num_seqs,
+                           int32_t* block_tables, int64_t block_tables_stride, int block_size,
+                           int64_t num_blocks, const int32_t* free_ring, int64_t ring_size,
+                           const int64_t* ring_state, int64_t* ring_state_out,
+                           int64_t num_tokens, int32_t* query_start_loc,
+                           int32_t* block_start_loc, int32_t* seq_lens, int64_t* positions,
+                           int64_t* slot_mapping, void* stream) {
+  if (num_seqs < 0 || num_seqs == 0x7fffffff || block_tables_stride < 0 || block_size <= 0 ||
+      num_blocks < 0 || ring_size < 0 || ring_size > 0x7fffffffll || num_tokens < 0 ||
+      num_tokens > 0x7fffffffll)
+    return PA_ERR_SHAPE;
+  if (!ring_state || !ring_state_out || !query_start_loc || !block_start_loc) return PA_ERR_NULL;
+  if (num_seqs > 0 && (!context_lens || !new_tokens || !seq_lens)) return PA_ERR_NULL;
+  if (num_seqs > 0 && block_tables_stride > 0 && !block_tables) return PA_ERR_NULL;
+  if (ring_size > 0 && !free_ring) return PA_ERR_NULL;
+  if (num_tokens > 0 && (!positions || !slot_mapping)) return PA_ERR_NULL;
+  if (!aligned(context_lens, 4) || !aligned(new_tokens, 4) || !aligned(block_tables, 4) ||
+      !aligned(free_ring, 4) || !aligned(query_start_loc, 4) || !aligned(block_start_loc, 4) ||
+      !aligned(seq_lens, 4) || !aligned(ring_state, 8) || !aligned(ring_state_out, 8) ||
+      !aligned(positions, 8) || !aligned(slot_mapping, 8))
+    return PA_ERR_ALIGN;
+  int dev;
+  int st = device_setup(&dev);
+  if (st != PA_OK) return st;
+  const pa::ExtendArgs a{context_lens, new_tokens, num_seqs, block_tables, block_tables_stride,
+                         block_size, num_blocks, free_ring, ring_size, ring_state,
+                         ring_state_out, num_tokens, query_start_loc, block_start_loc, seq_lens,
+                         positions, slot_mapping, g_err_ptr[dev]};
+  return check_launch(pa::launch_extend_tables(a, g_sm_count[dev], (cudaStream_t)stream));
+}
+
+int pa_release_block_tables(const uint8_t* finished, const int32_t* seq_lens, int num_seqs,
+                            const int32_t* block_tables, int64_t block_tables_stride,
+                            int block_size, int64_t num_blocks, int32_t* free_ring,
+                            int64_t ring_size, const int64_t* ring_state,
+                            int64_t* ring_state_out, int32_t* release_start_loc,
+                            int32_t* seq_lens_out, void* stream) {
+  if (num_seqs < 0 || num_seqs == 0x7fffffff || block_tables_stride < 0 || block_size <= 0 ||
+      num_blocks < 0 || ring_size < 0 || ring_size > 0x7fffffffll)
+    return PA_ERR_SHAPE;
+  if (!ring_state || !ring_state_out || !release_start_loc) return PA_ERR_NULL;
+  if (num_seqs > 0 && (!finished || !seq_lens || !seq_lens_out)) return PA_ERR_NULL;
+  if (num_seqs > 0 && block_tables_stride > 0 && !block_tables) return PA_ERR_NULL;
+  if (ring_size > 0 && !free_ring) return PA_ERR_NULL;
+  if (!aligned(seq_lens, 4) || !aligned(block_tables, 4) || !aligned(free_ring, 4) ||
+      !aligned(release_start_loc, 4) || !aligned(seq_lens_out, 4) || !aligned(ring_state, 8) ||
+      !aligned(ring_state_out, 8))
+    return PA_ERR_ALIGN;
+  int dev;
+  int st = device_setup(&dev);
+  if (st != PA_OK) return st;
+  const pa::ReleaseArgs a{finished, seq_lens, num_seqs, block_tables, block_tables_stride,
+                          block_size, num_blocks, free_ring, ring_size, ring_state,
+                          ring_state_out, release_start_loc, seq_lens_out, g_err_ptr[dev]};
+  return check_launch(pa::launch_release_tables(a, g_sm_count[dev], (cudaStream_t)stream));
+}
+
+int pa_rotary_reshape_and_cache(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+    int dtype, const int64_t* positions, int64_t position_stride, int num_axes,
+    const double* inv_freq, const int32_t* axis_of_pair, int rot_size, int interleaved,
+    const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* key_cache,
+    void* value_cache, int64_t num_blocks, int block_size, void* stream) {
+  pa::RotaryArgs a{q, k, v, q_stride, k_stride, v_stride, num_tokens, num_q_heads, num_kv_heads,
+                   head_size, dtype, positions, position_stride, num_axes, inv_freq,
+                   axis_of_pair, rot_size, interleaved, slot_mapping, q_out, q_out_stride,
+                   key_cache, value_cache, num_blocks, block_size, 0, 1.f, 1.f, nullptr, nullptr,
+                   nullptr};
+  return run_rotary(a, stream);
+}
+
+int pa_rotary_reshape_and_cache_fp8(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+    int dtype, const int64_t* positions, int64_t position_stride, int num_axes,
+    const double* inv_freq, const int32_t* axis_of_pair, int rot_size, int interleaved,
+    const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* key_cache,
+    void* value_cache, int64_t num_blocks, int block_size, float k_scale, float v_scale,
+    void* stream) {
+  if (!(k_scale > 0.f) || !(v_scale > 0.f)) return PA_ERR_SHAPE;
+  pa::RotaryArgs a{q, k, v, q_stride, k_stride, v_stride, num_tokens, num_q_heads, num_kv_heads,
+                   head_size, dtype, positions, position_stride, num_axes, inv_freq,
+                   axis_of_pair, rot_size, interleaved, slot_mapping, q_out, q_out_stride,
+                   key_cache, value_cache, num_blocks, block_size, 1, k_scale, v_scale, nullptr,
+                   nullptr, nullptr};
+  return run_rotary(a, stream);
+}
+
+int pa_rotary_reshape_and_cache_fp8_scaled(
+    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+    int64_t v_stride, int64_t num_tokens, int num_q_heads, int num_kv_heads, int head_size,
+    int dtype, const int64_t* positions, int64_t position_stride, int num_axes,
+    const double* inv_freq, const int32_t* axis_of_pair, int rot_size, int interleaved,
+    const int64_t* slot_mapping, void* q_out, int64_t q_out_stride, void* key_cache,
+    void* value_cache, int64_t num_blocks, int block_size, float* k_scales, float* v_scales,
+    void* stream) {
+  if (num_tokens > 0 && (!k_scales || !v_scales)) return PA_ERR_NULL;
+  if (!aligned16(k_scales) || !aligned16(v_scales)) return PA_ERR_ALIGN;
+  pa::RotaryArgs a{q, k, v, q_stride, k_stride, v_stride, num_tokens, num_q_heads, num_kv_heads,
+                   head_size, dtype, positions, position_stride, num_axes, inv_freq,
+                   axis_of_pair, rot_size, interleaved, slot_mapping, q_out, q_out_stride,
+                   key_cache, value_cache, num_blocks, block_size, 1, 1.f, 1.f, k_scales,
+                   v_scales, nullptr};
+  return run_rotary(a, stream);
+}
+
 int pa_get_device_error(int* code_out, void* stream) {
   if (!code_out) return PA_ERR_NULL;
   int dev;
@@ -816,6 +929,41 @@ int run_decode(const void* q, const void* key_cache, const void* value_cache,
   cudaStream_t cs = (cudaStream_t)stream;
   return check_launch(fp8 ? pa::launch_decode_fp8(a, k_scale, v_scale, cs)
                           : pa::launch_decode(a, cs));
+}
+
+// Validation and launch shared by the rotary KV writes.
+int run_rotary(pa::RotaryArgs& a, void* stream) {
+  const int eb = elt_bytes(a.dtype);
+  if (eb == 0) return PA_ERR_DTYPE;
+  if (a.num_tokens < 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.block_size <= 0 ||
+      a.num_blocks < 0 || a.num_axes < 1 || a.num_axes > 8)
+    return PA_ERR_SHAPE;
+  if (a.head_size <= 0 || a.head_size > 256 || a.head_size % 16 != 0 || a.rot_size <= 0 ||
+      a.rot_size > a.head_size || a.rot_size % 16 != 0)
+    return PA_ERR_SHAPE;
+  if ((int64_t)a.num_q_heads + 2 * (int64_t)a.num_kv_heads > 0x7fffff) return PA_ERR_SHAPE;
+  const int64_t q_row = (int64_t)a.num_q_heads * a.head_size;
+  const int64_t kv_row = (int64_t)a.num_kv_heads * a.head_size;
+  if (a.q_stride < q_row || a.q_out_stride < q_row || a.k_stride < kv_row || a.v_stride < kv_row ||
+      a.position_stride < (a.num_axes > 1 ? a.num_tokens : 0))
+    return PA_ERR_SHAPE;
+  if (a.num_tokens == 0) return PA_OK;
+  if (!a.q || !a.k || !a.v || !a.positions || !a.inv_freq || !a.slots || !a.q_out || !a.kc ||
+      !a.vc)
+    return PA_ERR_NULL;
+  if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q_out) ||
+      !aligned16(a.kc) || !aligned16(a.vc) || !aligned(a.positions, 8) ||
+      !aligned(a.inv_freq, 8) || !aligned(a.axis_of_pair, 4) || !aligned(a.slots, 8))
+    return PA_ERR_ALIGN;
+  if (a.q_stride * eb % 16 != 0 || a.k_stride * eb % 16 != 0 || a.v_stride * eb % 16 != 0 ||
+      a.q_out_stride * eb % 16 != 0)
+    return PA_ERR_ALIGN;
+  if (a.q == a.q_out && a.q_stride != a.q_out_stride) return PA_ERR_ALIAS;
+  int dev;
+  const int st = device_setup(&dev);
+  if (st != PA_OK) return st;
+  a.err = g_err_ptr[dev];
+  return check_launch(pa::launch_rotary(a, g_sm_count[dev], (cudaStream_t)stream));
 }
 
 }  // namespace

@@ -34,6 +34,72 @@ cudaError_t launch_map_to_kernel_blocks(const int32_t* mtab, int64_t rows, int64
                                         int64_t cols, int r, int32_t* ktab, int64_t kstride,
                                         int sm_count, cudaStream_t st, int* err);
 
+// Step bookkeeping on the GPU (step_tables.cu).
+struct ExtendArgs {
+  const int32_t* context_lens;
+  const int32_t* new_tokens;
+  int num_seqs;
+  int32_t* block_tables;
+  int64_t table_stride;
+  int block_size;
+  int64_t num_blocks;
+  const int32_t* free_ring;
+  int64_t ring_size;
+  const int64_t* ring_state;    // head, tail
+  int64_t* ring_state_out;      // may be ring_state
+  int64_t num_tokens;           // rows of positions / slot_mapping
+  int32_t* query_start_loc;     // [num_seqs + 1]
+  int32_t* block_start_loc;     // [num_seqs + 1]
+  int32_t* seq_lens;            // may be context_lens
+  int64_t* positions;
+  int64_t* slot_mapping;
+  int* err;
+};
+cudaError_t launch_extend_tables(const ExtendArgs& a, int sm_count, cudaStream_t st);
+
+struct ReleaseArgs {
+  const uint8_t* finished;
+  const int32_t* seq_lens;
+  int num_seqs;
+  const int32_t* block_tables;
+  int64_t table_stride;
+  int block_size;
+  int64_t num_blocks;
+  int32_t* free_ring;
+  int64_t ring_size;
+  const int64_t* ring_state;
+  int64_t* ring_state_out;      // may be ring_state
+  int32_t* release_start_loc;   // [num_seqs + 1]
+  int32_t* seq_lens_out;        // may be seq_lens
+  int* err;
+};
+cudaError_t launch_release_tables(const ReleaseArgs& a, int sm_count, cudaStream_t st);
+
+// Rotary positions fused with the KV write (rotary.cu).
+struct RotaryArgs {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;   // elements between tokens
+  int64_t num_tokens;
+  int num_q_heads, num_kv_heads, head_size, dtype;
+  const int64_t* positions;               // [num_axes][num_tokens]
+  int64_t position_stride;
+  int num_axes;
+  const double* inv_freq;                 // [rot_size / 2]
+  const int32_t* axis_of_pair;            // [rot_size / 2]; nullptr: axis 0
+  int rot_size, interleaved;
+  const int64_t* slots;
+  void* q_out;
+  int64_t q_out_stride;
+  void *kc, *vc;
+  int64_t num_blocks;
+  int block_size;
+  int pool;                               // 0: pools of dtype, 1: E4M3 pools
+  float k_scale, v_scale;                 // pool 1, one scale per pool
+  float *k_scales, *v_scales;             // pool 1, per-block scales, or nullptr
+  int* err;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int sm_count, cudaStream_t st);
+
 struct DecodeArgs {
   const void* q;
   const void* kc;

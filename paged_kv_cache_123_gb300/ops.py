@@ -452,6 +452,207 @@ def pa_decode_attention_fp8_window(q: torch.Tensor, key_cache: torch.Tensor,
                         window, out, max_seq_len, partition_size, workspace, stream)
 
 
+def _here(t: torch.Tensor, name: str, dtype=None, shape=None, dense=True):
+    """_dev plus the current device and the shape; dense=False leaves the
+    strides to the caller."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if dense and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _buffer(t, name, dtype, shape, device):
+    """The caller's output buffer, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _here(t, name, dtype, shape)
+    return t
+
+
+def pa_extend_block_tables(context_lens: torch.Tensor, new_tokens: torch.Tensor,
+                           block_tables: torch.Tensor, block_size: int, free_ring: torch.Tensor,
+                           ring_state: torch.Tensor, num_blocks: int, num_tokens: int, *,
+                           ring_state_out: Optional[torch.Tensor] = None,
+                           query_start_loc: Optional[torch.Tensor] = None,
+                           block_start_loc: Optional[torch.Tensor] = None,
+                           seq_lens: Optional[torch.Tensor] = None,
+                           positions: Optional[torch.Tensor] = None,
+                           slot_mapping: Optional[torch.Tensor] = None, stream=None):
+    """Plan a step on the GPU: request r holds context_lens[r] tokens and gets
+    new_tokens[r] more (int32 [S]); the blocks it lacks come from the head of
+    the free ring (free_ring int32 [R], ring_state int64 {head, tail}) and are
+    entered in block_tables (int32 [S, max_blocks]). num_tokens rows (an upper
+    bound of the new tokens) of positions and slots are written, padding rows
+    with slot -1. ring_state_out defaults to ring_state (in place); seq_lens
+    may be context_lens. Returns (query_start_loc, block_start_loc, seq_lens,
+    positions, slot_mapping). A step that lacks blocks changes nothing and
+    latches PA_ERR_NO_BLOCKS."""
+    S, dev = context_lens.numel(), context_lens.device
+    i32, i64 = torch.int32, torch.int64
+    _here(context_lens, "context_lens", i32, (S,))
+    _here(new_tokens, "new_tokens", i32, (S,))
+    _here(block_tables, "block_tables", i32)
+    _here(free_ring, "free_ring", i32)
+    _here(ring_state, "ring_state", i64, (2,))
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    T = int(num_tokens)
+    if T < 0:
+        raise ValueError("num_tokens must not be negative")
+    ring_state_out = (ring_state if ring_state_out is None else
+                      _buffer(ring_state_out, "ring_state_out", i64, (2,), dev))
+    query_start_loc = _buffer(query_start_loc, "query_start_loc", i32, (S + 1,), dev)
+    block_start_loc = _buffer(block_start_loc, "block_start_loc", i32, (S + 1,), dev)
+    seq_lens = _buffer(seq_lens, "seq_lens", i32, (S,), dev)
+    positions = _buffer(positions, "positions", i64, (T,), dev)
+    slot_mapping = _buffer(slot_mapping, "slot_mapping", i64, (T,), dev)
+    check("pa_extend_block_tables", lib().pa_extend_block_tables(
+        ptr(context_lens), ptr(new_tokens), S, ptr(block_tables), block_tables.shape[1],
+        int(block_size), int(num_blocks), ptr(free_ring), free_ring.numel(), ptr(ring_state),
+        ptr(ring_state_out), T, ptr(query_start_loc), ptr(block_start_loc), ptr(seq_lens),
+        ptr(positions), ptr(slot_mapping), stream_handle(stream)))
+    return query_start_loc, block_start_loc, seq_lens, positions, slot_mapping
+
+
+def pa_release_block_tables(finished: torch.Tensor, seq_lens: torch.Tensor,
+                            block_tables: torch.Tensor, block_size: int,
+                            free_ring: torch.Tensor, ring_state: torch.Tensor, num_blocks: int, *,
+                            ring_state_out: Optional[torch.Tensor] = None,
+                            release_start_loc: Optional[torch.Tensor] = None,
+                            seq_lens_out: Optional[torch.Tensor] = None,
+                            stream=None) -> torch.Tensor:
+    """Return the blocks of finished requests (uint8 or bool [S]) to the tail
+    of the free ring and set their lengths to 0. ring_state_out and
+    seq_lens_out default to in place. Returns release_start_loc int32 [S + 1]:
+    where each request's blocks begin among those returned."""
+    S, dev = seq_lens.numel(), seq_lens.device
+    i32, i64 = torch.int32, torch.int64
+    if finished.dtype == torch.bool:
+        finished = finished.view(torch.uint8)
+    _here(finished, "finished", torch.uint8, (S,))
+    _here(seq_lens, "seq_lens", i32, (S,))
+    _here(block_tables, "block_tables", i32)
+    _here(free_ring, "free_ring", i32)
+    _here(ring_state, "ring_state", i64, (2,))
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    ring_state_out = (ring_state if ring_state_out is None else
+                      _buffer(ring_state_out, "ring_state_out", i64, (2,), dev))
+    seq_lens_out = (seq_lens if seq_lens_out is None else
+                    _buffer(seq_lens_out, "seq_lens_out", i32, (S,), dev))
+    release_start_loc = _buffer(release_start_loc, "release_start_loc", i32, (S + 1,), dev)
+    check("pa_release_block_tables", lib().pa_release_block_tables(
+        ptr(finished), ptr(seq_lens), S, ptr(block_tables), block_tables.shape[1],
+        int(block_size), int(num_blocks), ptr(free_ring), free_ring.numel(), ptr(ring_state),
+        ptr(ring_state_out), ptr(release_start_loc), ptr(seq_lens_out), stream_handle(stream)))
+    return release_start_loc
+
+
+def _rows(t: torch.Tensor, name: str, shape, dtype):
+    """[T, H, D] whose tokens may be apart (a slice of a fused projection)."""
+    _here(t, name, dtype, shape, dense=False)
+    T, H, D = shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name} must have dense rows [heads, head_size]")
+    return t.stride(0) if T > 1 else H * D
+
+
+def _rotary_call(name, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
+                 pool_dtype, scales, axis_of_pair, interleaved, q_out, stream):
+    if q.dim() != 3 or k.dim() != 3 or key_cache.dim() != 4:
+        raise ValueError("q and k must be [T, heads, head_size], pools [NB, Hkv, B, D]")
+    T, Hq, D = q.shape
+    NB, Hkv, B, Dk = key_cache.shape
+    if Dk != D or value_cache.shape != key_cache.shape:
+        raise ValueError("pool shape does not match q")
+    if q.dtype not in DTYPE_CODE:
+        raise ValueError(f"q must be float32, float16 or bfloat16, got {q.dtype}")
+    qs = _rows(q, "q", (T, Hq, D), q.dtype)
+    ks = _rows(k, "k", (T, Hkv, D), q.dtype)
+    vs = _rows(v, "v", (T, Hkv, D), q.dtype)
+    _here(key_cache, "key_cache", pool_dtype)
+    _here(value_cache, "value_cache", pool_dtype)
+    _here(slot_mapping, "slot_mapping", torch.int64, (T,))
+    _here(positions, "positions", torch.int64)
+    if positions.shape[-1:] != (T,) or positions.dim() not in (1, 2):
+        raise ValueError("positions must be [T] or [axes, T]")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    half = inv_freq.numel()
+    _here(inv_freq, "inv_freq", torch.float64, (half,))
+    if axis_of_pair is not None:
+        _here(axis_of_pair, "axis_of_pair", torch.int32, (half,))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    qo = _rows(q_out, "q_out", (T, Hq, D), q.dtype)
+    check(name, getattr(lib(), name)(
+        ptr(q), qs, ptr(k), ks, ptr(v), vs, T, Hq, Hkv, D, DTYPE_CODE[q.dtype], ptr(positions), T,
+        axes, ptr(inv_freq), ptr(axis_of_pair), 2 * half, int(bool(interleaved)),
+        ptr(slot_mapping), ptr(q_out), qo, ptr(key_cache), ptr(value_cache), NB, B, *scales,
+        stream_handle(stream)))
+    return q_out
+
+
+def pa_rotary_reshape_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                positions: torch.Tensor, inv_freq: torch.Tensor,
+                                slot_mapping: torch.Tensor, key_cache: torch.Tensor,
+                                value_cache: torch.Tensor, *,
+                                axis_of_pair: Optional[torch.Tensor] = None,
+                                interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """Rotary positions of q [T, Hq, D] and k [T, Hkv, D] and the KV write in
+    one pass: pair i turns by positions[axis_of_pair[i], t] * inv_freq[i]
+    (positions int64 [T] or [axes, T]; inv_freq float64 [rot / 2];
+    axis_of_pair int32 [rot / 2], None: axis 0). q, k, v may be slices of one
+    projection (dense heads, any token stride). Writes rotated k and v into
+    the pools ([NB, Hkv, B, D], q's dtype) at slot_mapping and returns the
+    rotated q; q_out may be q."""
+    return _rotary_call("pa_rotary_reshape_and_cache", q, k, v, positions, inv_freq, slot_mapping,
+                        key_cache, value_cache, q.dtype, (), axis_of_pair, interleaved, q_out,
+                        stream)
+
+
+def pa_rotary_reshape_and_cache_fp8(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                    positions: torch.Tensor, inv_freq: torch.Tensor,
+                                    slot_mapping: torch.Tensor, key_cache: torch.Tensor,
+                                    value_cache: torch.Tensor, k_scale: float, v_scale: float, *,
+                                    axis_of_pair: Optional[torch.Tensor] = None,
+                                    interleaved: bool = False,
+                                    q_out: Optional[torch.Tensor] = None,
+                                    stream=None) -> torch.Tensor:
+    """pa_rotary_reshape_and_cache into E4M3 pools (uint8) with one scale per
+    pool; the fp32 rotated value is quantised."""
+    return _rotary_call("pa_rotary_reshape_and_cache_fp8", q, k, v, positions, inv_freq,
+                        slot_mapping, key_cache, value_cache, torch.uint8,
+                        (float(k_scale), float(v_scale)), axis_of_pair, interleaved, q_out,
+                        stream)
+
+
+def pa_rotary_reshape_and_cache_fp8_scaled(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                                           positions: torch.Tensor, inv_freq: torch.Tensor,
+                                           slot_mapping: torch.Tensor, key_cache: torch.Tensor,
+                                           value_cache: torch.Tensor, k_scales: torch.Tensor,
+                                           v_scales: torch.Tensor, *,
+                                           axis_of_pair: Optional[torch.Tensor] = None,
+                                           interleaved: bool = False,
+                                           q_out: Optional[torch.Tensor] = None,
+                                           stream=None) -> torch.Tensor:
+    """pa_rotary_reshape_and_cache into E4M3 pools whose blocks carry their
+    own scales (float32 [NB, Hkv]), updated where this write stores a block's
+    first row."""
+    want = tuple(key_cache.shape[:2])
+    _here(k_scales, "k_scales", torch.float32, want)
+    _here(v_scales, "v_scales", torch.float32, want)
+    return _rotary_call("pa_rotary_reshape_and_cache_fp8_scaled", q, k, v, positions, inv_freq,
+                        slot_mapping, key_cache, value_cache, torch.uint8,
+                        (ptr(k_scales), ptr(v_scales)), axis_of_pair, interleaved, q_out, stream)
+
+
 def pa_selftest_bounded_wait(timeout_cycles: int = 2_000_000, stream=None) -> list:
     """Run the bounded-wait self-test; returns [status of warp 0, status of
     warp 1, abort flag] (expected: [PA_ERR_TIMEOUT, PA_ERR_TIMEOUT, 1])."""
