@@ -522,6 +522,60 @@ PA_API int pa_decode_attention_fp8_scaled(const void* q, const void* key_cache,
                                           int64_t workspace_bytes, void* stream);
 
 /*
+ * Several new tokens per sequence over fp8 (E4M3) pools: prefill chunks,
+ * speculative tokens and single tokens in one batch, with an optional
+ * sliding window, so that a prompt can be prefilled chunk by chunk into an
+ * fp8 pool.
+ *
+ * pa_multi_query_attention_fp8 — pa_multi_query_attention with K = code *
+ * k_scale and V = code * v_scale (both > 0). window = W > 0: the new token at
+ * position p attends to positions max(0, p - W + 1) .. p; table entries of
+ * blocks that no new token's window reaches are never read (they may be
+ * released, e.g. -1). window = 0 is plain causal attention.
+ * pa_multi_query_attention_fp8_scaled — blocks that carry their own scales,
+ * k_scales and v_scales float32 [num_blocks][num_kv_heads] as the scaled
+ * writes leave them.
+ *
+ * q, out, query_start_loc, seq_lens, max_query_len, max_seq_len, shapes,
+ * errors: as in pa_multi_query_attention (fp16/bf16 queries, head_size 64 or
+ * 128, block_size a power of two in [8, 256], group 1/2/4/8). Rows of out
+ * that belong to no sequence, or to one whose lengths are out of range, are
+ * not written. Products are fp16 x fp16 with fp32 accumulation: the codes
+ * are exact in fp16, a bf16 query row is scaled by a power of two so that
+ * its values are exact down to 2^-24 of the largest (an element below that
+ * is rounded there). A masked token never reaches a row, whatever its K and
+ * V hold (NaN included).
+ * A V scale more than 2^24 below the largest of the sequence loses weight
+ * precision, as in pa_decode_attention_fp8_scaled.
+ * partition_size  tokens per partition of the keys that one tile of 128
+ *               (token, query head) rows spans, rounded up to 128; 0 picks one from
+ *               the SM count. Results are reproducible bit for bit for
+ *               fixed arguments.
+ *
+ * pa_multi_query_fp8_workspace_bytes — scratch for both calls with the same
+ * arguments (0: NULL may be passed; negative status on invalid sizes).
+ */
+PA_API int64_t pa_multi_query_fp8_workspace_bytes(int64_t num_tokens, int num_seqs,
+                                                  int num_q_heads, int num_kv_heads,
+                                                  int head_size, int block_size,
+                                                  int max_query_len, int max_seq_len,
+                                                  int window, int partition_size);
+PA_API int pa_multi_query_attention_fp8(
+    const void* q, const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+    const void* key_cache, const void* value_cache, const int32_t* block_tables,
+    int64_t block_tables_stride, const int32_t* seq_lens, int num_q_heads, int num_kv_heads,
+    int head_size, int block_size, int64_t num_blocks, int dtype, float scale, float k_scale,
+    float v_scale, int window, int max_query_len, int max_seq_len, int partition_size, void* out,
+    void* workspace, int64_t workspace_bytes, void* stream);
+PA_API int pa_multi_query_attention_fp8_scaled(
+    const void* q, const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+    const void* key_cache, const void* value_cache, const float* k_scales, const float* v_scales,
+    const int32_t* block_tables, int64_t block_tables_stride, const int32_t* seq_lens,
+    int num_q_heads, int num_kv_heads, int head_size, int block_size, int64_t num_blocks, int dtype,
+    float scale, int window, int max_query_len, int max_seq_len, int partition_size, void* out,
+    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
  * Sliding-window decode. The pages name the window through the blocks the
  * allocator may release ("PagedAttention 核心创新深度分析" §3.2
  * allocate_slots, phase 1, and §3.3.1 get_num_blocks_to_allocate: skipped

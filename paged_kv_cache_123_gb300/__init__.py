@@ -17,6 +17,8 @@ from .ops import (  # noqa: F401
     pa_decode_attention_fp8_scaled, pa_decode_fp8_workspace_bytes, pa_decode_even_ctas,
     pa_extend_block_tables, pa_release_block_tables, pa_rotary_reshape_and_cache,
     pa_rotary_reshape_and_cache_fp8, pa_rotary_reshape_and_cache_fp8_scaled,
+    pa_multi_query_attention_fp8, pa_multi_query_attention_fp8_scaled,
+    pa_multi_query_fp8_workspace_bytes,
 )
 from ._lib import PagedAttnError, LIB_PATH, lib  # noqa: F401
 from .block_pool import BlockPool  # noqa: F401

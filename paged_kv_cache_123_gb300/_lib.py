@@ -77,6 +77,13 @@ _ROTARY = ([_c_p, _c_i64] * 3 + [_c_i64] + [_c_i32] * 4 + [_c_p, _c_i64, _c_i32,
                                                            _c_i32, _c_i32, _c_p, _c_p, _c_i64,
                                                            _c_p, _c_p, _c_i64, _c_i32])
 SIGNATURES.update({
+    "pa_multi_query_fp8_workspace_bytes": ([_c_i64] + [_c_i32] * 9, _c_i64),
+    "pa_multi_query_attention_fp8": ([_c_p, _c_p, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_i64, _c_p]
+                                     + [_c_i32] * 4 + [_c_i64, _c_i32, _c_f, _c_f, _c_f]
+                                     + [_c_i32] * 4 + [_c_p, _c_p, _c_i64, _c_p], _c_i32),
+    "pa_multi_query_attention_fp8_scaled": (
+        [_c_p, _c_p, _c_i32, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p] + [_c_i32] * 4
+        + [_c_i64, _c_i32, _c_f] + [_c_i32] * 4 + [_c_p, _c_p, _c_i64, _c_p], _c_i32),
     "pa_extend_block_tables": ([_c_p, _c_p, _c_i32, _c_p, _c_i64, _c_i32, _c_i64, _c_p, _c_i64,
                                 _c_p, _c_p, _c_i64] + [_c_p] * 6, _c_i32),
     "pa_release_block_tables": ([_c_p, _c_p, _c_i32, _c_p, _c_i64, _c_i32, _c_i64, _c_p, _c_i64]

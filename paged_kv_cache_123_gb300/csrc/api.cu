@@ -60,6 +60,20 @@ int elt_bytes(int dtype) {
 
 int run_rotary(pa::RotaryArgs& a, void* stream);
 
+// partial outputs [num_tokens][Hq][splits][D], maxima and sums [..][splits][2]
+int64_t chunk_workspace(int64_t num_tokens, int num_q_heads, int head_size, int splits) {
+  if (splits <= 1) return 0;
+  const int64_t n = num_tokens * num_q_heads * splits;
+  return ((n * head_size * 4 + 255) / 256) * 256 + n * 2 * 4;
+}
+int run_chunk(const void* q, const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+              const void* key_cache, const void* value_cache, const float* k_scales,
+              const float* v_scales, float k_scale, float v_scale, const int32_t* block_tables,
+              int64_t block_tables_stride, const int32_t* seq_lens, int num_q_heads,
+              int num_kv_heads, int head_size, int block_size, int64_t num_blocks, int dtype,
+              float scale, int window, int max_query_len, int max_seq_len, int partition_size,
+              void* out, void* workspace, int64_t workspace_bytes, void* stream);
+
 int check_launch(cudaError_t e) {
   if (e == cudaSuccess) return PA_OK;
   if (e == cudaErrorNoKernelImageForDevice || e == cudaErrorInvalidDeviceFunction)
@@ -585,6 +599,55 @@ int pa_multi_query_attention(const void* q, const int32_t* query_start_loc, int 
   return check_launch(pa::launch_multi_query(a, (cudaStream_t)stream));
 }
 
+int64_t pa_multi_query_fp8_workspace_bytes(int64_t num_tokens, int num_seqs, int num_q_heads,
+                                           int num_kv_heads, int head_size, int block_size,
+                                           int max_query_len, int max_seq_len, int window,
+                                           int partition_size) {
+  int st = check_mq_shape(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                          max_query_len, max_seq_len);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0 || num_tokens > 0x7fffffffll || window < 0 || partition_size < 0)
+    return PA_ERR_SHAPE;
+  int dev;
+  st = device_setup(&dev);
+  if (st != PA_OK) return st;
+  int splits, tokens;
+  pa::chunk_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_seq_len,
+                 window, partition_size, g_sm_count[dev], &splits, &tokens);
+  return chunk_workspace(num_tokens, num_q_heads, head_size, splits);
+}
+
+int pa_multi_query_attention_fp8(
+    const void* q, const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+    const void* key_cache, const void* value_cache, const int32_t* block_tables,
+    int64_t block_tables_stride, const int32_t* seq_lens, int num_q_heads, int num_kv_heads,
+    int head_size, int block_size, int64_t num_blocks, int dtype, float scale, float k_scale,
+    float v_scale, int window, int max_query_len, int max_seq_len, int partition_size, void* out,
+    void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!(k_scale > 0.f) || !(v_scale > 0.f)) return PA_ERR_SHAPE;
+  return run_chunk(q, query_start_loc, num_seqs, num_tokens, key_cache, value_cache, nullptr,
+                   nullptr, k_scale, v_scale, block_tables, block_tables_stride, seq_lens,
+                   num_q_heads, num_kv_heads, head_size, block_size, num_blocks, dtype, scale,
+                   window, max_query_len, max_seq_len, partition_size, out, workspace,
+                   workspace_bytes, stream);
+}
+
+int pa_multi_query_attention_fp8_scaled(
+    const void* q, const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+    const void* key_cache, const void* value_cache, const float* k_scales, const float* v_scales,
+    const int32_t* block_tables, int64_t block_tables_stride, const int32_t* seq_lens,
+    int num_q_heads, int num_kv_heads, int head_size, int block_size, int64_t num_blocks, int dtype,
+    float scale, int window, int max_query_len, int max_seq_len, int partition_size, void* out,
+    void* workspace, int64_t workspace_bytes, void* stream) {
+  if (num_seqs > 0 && (!k_scales || !v_scales)) return PA_ERR_NULL;
+  if (!aligned16(k_scales) || !aligned16(v_scales)) return PA_ERR_ALIGN;
+  return run_chunk(q, query_start_loc, num_seqs, num_tokens, key_cache, value_cache, k_scales,
+                   v_scales, 1.f, 1.f, block_tables, block_tables_stride, seq_lens, num_q_heads,
+                   num_kv_heads, head_size, block_size, num_blocks, dtype, scale, window,
+                   max_query_len, max_seq_len, partition_size, out, workspace, workspace_bytes,
+                   stream);
+}
+
 int pa_reshape_and_cache_fp8(const void* k, const void* v, int64_t num_tokens, int num_kv_heads,
                              int head_size, int dtype, const int64_t* slot_mapping,
                              void* key_cache, void* value_cache, int64_t num_blocks,
@@ -964,6 +1027,58 @@ int run_rotary(pa::RotaryArgs& a, void* stream) {
   if (st != PA_OK) return st;
   a.err = g_err_ptr[dev];
   return check_launch(pa::launch_rotary(a, g_sm_count[dev], (cudaStream_t)stream));
+}
+
+// Validation, partitioning and launch shared by the fp8 multi-query calls.
+int run_chunk(const void* q, const int32_t* query_start_loc, int num_seqs, int64_t num_tokens,
+              const void* key_cache, const void* value_cache, const float* k_scales,
+              const float* v_scales, float k_scale, float v_scale, const int32_t* block_tables,
+              int64_t block_tables_stride, const int32_t* seq_lens, int num_q_heads,
+              int num_kv_heads, int head_size, int block_size, int64_t num_blocks, int dtype,
+              float scale, int window, int max_query_len, int max_seq_len, int partition_size,
+              void* out, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (dtype != PA_F16 && dtype != PA_BF16) return elt_bytes(dtype) ? PA_ERR_SHAPE : PA_ERR_DTYPE;
+  int st = check_mq_shape(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
+                          max_query_len, max_seq_len);
+  if (st != PA_OK) return st;
+  if (num_blocks < 0 || num_blocks * num_kv_heads > 0x7fffffffll || block_tables_stride < 0 ||
+      num_tokens < 0 || num_tokens > 0x7fffffffll || partition_size < 0 || window < 0 ||
+      num_q_heads > 65535)
+    return PA_ERR_SHAPE;
+  if ((int64_t)max_seq_len > block_tables_stride * block_size) return PA_ERR_OUT_OF_RANGE;
+  if (num_seqs == 0 || max_query_len == 0 || num_tokens == 0) return PA_OK;
+  if (num_blocks == 0) return PA_ERR_SHAPE;
+  if (!q || !query_start_loc || !key_cache || !value_cache || !block_tables || !seq_lens || !out)
+    return PA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(key_cache) || !aligned16(value_cache) || !aligned16(out) ||
+      !aligned(query_start_loc, 4) || !aligned(block_tables, 4) || !aligned(seq_lens, 4))
+    return PA_ERR_ALIGN;
+  int dev;
+  st = device_setup(&dev);
+  if (st != PA_OK) return st;
+  pa::ChunkArgs a;
+  a.q = q; a.qsl = query_start_loc; a.num_seqs = num_seqs; a.num_tokens = num_tokens;
+  a.kc = key_cache; a.vc = value_cache; a.tables = block_tables;
+  a.table_stride = block_tables_stride; a.seq_lens = seq_lens;
+  a.num_q_heads = num_q_heads; a.num_kv_heads = num_kv_heads; a.head_size = head_size;
+  a.block_size = block_size; a.num_blocks = num_blocks; a.dtype = dtype; a.scale = scale;
+  a.max_query_len = max_query_len; a.max_seq_len = max_seq_len; a.out = out;
+  a.window = window; a.k_scale = k_scale; a.v_scale = v_scale;
+  a.k_scales = k_scales; a.v_scales = v_scales;
+  pa::chunk_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_seq_len,
+                 window, partition_size, g_sm_count[dev], &a.num_splits, &a.partition);
+  a.ws_acc = nullptr; a.ws_ml = nullptr;
+  const int64_t need = chunk_workspace(num_tokens, num_q_heads, head_size, a.num_splits);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need) return PA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return PA_ERR_ALIGN;
+    const int64_t n = num_tokens * num_q_heads * a.num_splits;
+    a.ws_acc = static_cast<float*>(workspace);
+    a.ws_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                       ((n * head_size * 4 + 255) / 256) * 256);
+  }
+  a.err = g_err_ptr[dev];
+  return check_launch(pa::launch_chunk_fp8(a, (cudaStream_t)stream));
 }
 
 }  // namespace

@@ -653,6 +653,95 @@ def pa_rotary_reshape_and_cache_fp8_scaled(q: torch.Tensor, k: torch.Tensor, v: 
                         (ptr(k_scales), ptr(v_scales)), axis_of_pair, interleaved, q_out, stream)
 
 
+def pa_multi_query_fp8_workspace_bytes(num_tokens: int, num_seqs: int, num_q_heads: int,
+                                       num_kv_heads: int, head_size: int, block_size: int,
+                                       max_query_len: int, max_seq_len: int, window: int = 0,
+                                       partition_size: int = 0) -> int:
+    """Scratch bytes of the fp8-pool multi-query calls with these sizes."""
+    n = lib().pa_multi_query_fp8_workspace_bytes(num_tokens, num_seqs, num_q_heads, num_kv_heads,
+                                                 head_size, block_size, max_query_len,
+                                                 max_seq_len, window, partition_size)
+    if n < 0:
+        check("pa_multi_query_fp8_workspace_bytes", int(n))
+    return int(n)
+
+
+def _chunk_call(name, q, query_start_loc, key_cache, value_cache, scale_tensors, scale_values,
+                block_tables, seq_lens, scale, num_kv_heads, out, max_query_len, max_seq_len,
+                window, partition_size, workspace, stream):
+    if q.dim() != 3 or key_cache.dim() != 4 or block_tables.dim() != 2:
+        raise ValueError("q must be [T, Hq, D], pools [NB, Hkv, B, D], block_tables [S, blocks]")
+    T, Hq, D = q.shape
+    NB, Hkv, B, Dk = key_cache.shape
+    S = seq_lens.numel()
+    if q.dtype not in DTYPE_CODE:
+        raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
+    if Hkv != num_kv_heads or Dk != D or value_cache.shape != key_cache.shape:
+        raise ValueError("pool shape does not match q / num_kv_heads")
+    _here(q, "q")
+    _here(key_cache, "key_cache", torch.uint8)
+    _here(value_cache, "value_cache", torch.uint8)
+    _here(query_start_loc, "query_start_loc", torch.int32, (S + 1,))
+    _here(seq_lens, "seq_lens", torch.int32, (S,))
+    _here(block_tables, "block_tables", torch.int32)
+    if block_tables.shape[0] != S:
+        raise ValueError("block_tables must have one row per sequence")
+    for t in scale_tensors:
+        _here(t, "scales", torch.float32, (NB, Hkv))
+    out = _buffer(out, "out", q.dtype, (T, Hq, D), q.device)
+    if workspace is None:
+        need = pa_multi_query_fp8_workspace_bytes(T, S, Hq, Hkv, D, B, max_query_len, max_seq_len,
+                                                  window, partition_size)
+        if need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    else:
+        _here(workspace, "workspace")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(name, getattr(lib(), name)(
+        ptr(q), ptr(query_start_loc), S, T, ptr(key_cache), ptr(value_cache),
+        *[ptr(t) for t in scale_tensors], ptr(block_tables), block_tables.shape[1], ptr(seq_lens),
+        Hq, Hkv, D, B, NB, DTYPE_CODE[q.dtype], float(scale), *scale_values, int(window),
+        int(max_query_len), int(max_seq_len), int(partition_size), ptr(out), ptr(workspace),
+        ws_bytes, stream_handle(stream)))
+    return out
+
+
+def pa_multi_query_attention_fp8(q: torch.Tensor, query_start_loc: torch.Tensor,
+                                 key_cache: torch.Tensor, value_cache: torch.Tensor,
+                                 block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                 scale: float, num_kv_heads: int, k_scale: float, v_scale: float,
+                                 out: Optional[torch.Tensor] = None, *, max_query_len: int,
+                                 max_seq_len: int, window: int = 0, partition_size: int = 0,
+                                 workspace: Optional[torch.Tensor] = None,
+                                 stream=None) -> torch.Tensor:
+    """pa_multi_query_attention over E4M3 pools (uint8 [NB, Hkv, B, D]) with
+    one scale per pool; window W > 0: the token at position p attends to
+    positions max(0, p - W + 1) .. p, and blocks before every window are
+    never looked up."""
+    return _chunk_call("pa_multi_query_attention_fp8", q, query_start_loc, key_cache, value_cache,
+                       (), (float(k_scale), float(v_scale)), block_tables, seq_lens, scale,
+                       num_kv_heads, out, max_query_len, max_seq_len, window, partition_size,
+                       workspace, stream)
+
+
+def pa_multi_query_attention_fp8_scaled(q: torch.Tensor, query_start_loc: torch.Tensor,
+                                        key_cache: torch.Tensor, value_cache: torch.Tensor,
+                                        k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                        block_tables: torch.Tensor, seq_lens: torch.Tensor,
+                                        scale: float, num_kv_heads: int,
+                                        out: Optional[torch.Tensor] = None, *,
+                                        max_query_len: int, max_seq_len: int, window: int = 0,
+                                        partition_size: int = 0,
+                                        workspace: Optional[torch.Tensor] = None,
+                                        stream=None) -> torch.Tensor:
+    """pa_multi_query_attention_fp8 over blocks that carry their own scales
+    (float32 [NB, Hkv] each)."""
+    return _chunk_call("pa_multi_query_attention_fp8_scaled", q, query_start_loc, key_cache,
+                       value_cache, (k_scales, v_scales), (), block_tables, seq_lens, scale,
+                       num_kv_heads, out, max_query_len, max_seq_len, window, partition_size,
+                       workspace, stream)
+
+
 def pa_selftest_bounded_wait(timeout_cycles: int = 2_000_000, stream=None) -> list:
     """Run the bounded-wait self-test; returns [status of warp 0, status of
     warp 1, abort flag] (expected: [PA_ERR_TIMEOUT, PA_ERR_TIMEOUT, 1])."""

@@ -95,3 +95,45 @@ def test_python_entry_points_want_cuda_tensors():
                                        kc)
     with pytest.raises(ValueError, match="head_size"):
         pa.pa_rotary_reshape_and_cache(q[0], q, q, st, st, st, kc, kc)
+
+
+CHUNK = dict(q=P, qsl=P, S=2, T=4, kc=P, vc=P, tables=P, stride=8, lens=P, Hq=8, Hkv=2, D=128,
+             B=16, NB=10, dtype=2, scale=0.1, k_scale=0.5, v_scale=0.5, window=0, max_q=4,
+             max_len=128, partition=0, out=P, ws=None, ws_bytes=0, stream=None)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(dtype=0), SHAPE), (dict(dtype=7), DTYPE), (dict(S=-1), SHAPE), (dict(T=-1), SHAPE),
+    (dict(T=1 << 31), SHAPE), (dict(Hq=6), SHAPE), (dict(Hq=32), SHAPE), (dict(D=96), SHAPE),
+    (dict(B=4), SHAPE), (dict(B=24), SHAPE), (dict(B=512), SHAPE), (dict(NB=-1), SHAPE),
+    (dict(NB=1 << 31), SHAPE), (dict(NB=0), SHAPE), (dict(window=-1), SHAPE),
+    (dict(max_q=-1), SHAPE), (dict(max_len=-1), SHAPE), (dict(partition=-1), SHAPE),
+    (dict(k_scale=0.0), SHAPE), (dict(v_scale=float("nan")), SHAPE), (dict(max_len=129), -5),
+    (dict(q=None), NULL), (dict(qsl=None), NULL), (dict(kc=None), NULL), (dict(vc=None), NULL),
+    (dict(tables=None), NULL), (dict(lens=None), NULL), (dict(out=None), NULL),
+    (dict(q=P + 8), ALIGN), (dict(kc=P + 1), ALIGN), (dict(out=P + 2), ALIGN),
+    (dict(qsl=P + 2), ALIGN)])
+def test_chunk_refusals(lib, change, status):
+    args = {**CHUNK, **change}
+    assert lib.pa_multi_query_attention_fp8(*args.values()) == status
+    if "k_scale" in change or "v_scale" in change:
+        return
+    vals = [v for k, v in args.items() if k not in ("k_scale", "v_scale")]
+    vals[6:6] = [P, P]
+    assert lib.pa_multi_query_attention_fp8_scaled(*vals) == status
+
+
+def test_chunk_needs_scales_and_nothing_for_no_rows(lib):
+    vals = [v for k, v in CHUNK.items() if k not in ("k_scale", "v_scale")]
+    assert lib.pa_multi_query_attention_fp8_scaled(*vals[:6], None, P, *vals[6:]) == NULL
+    assert lib.pa_multi_query_attention_fp8_scaled(*vals[:6], P, P + 4, *vals[6:]) == ALIGN
+    for change in (dict(S=0), dict(T=0), dict(max_q=0)):
+        assert lib.pa_multi_query_attention_fp8(*{**CHUNK, **change}.values()) == 0
+
+
+def test_chunk_workspace_refusals(lib):
+    good = [4, 2, 8, 2, 128, 16, 4, 128, 0, 0]
+    for at, bad in ((0, -1), (1, -1), (2, 6), (4, 100), (5, 4), (6, -1), (7, -1), (8, -1), (9, -1)):
+        args = list(good)
+        args[at] = bad
+        assert lib.pa_multi_query_fp8_workspace_bytes(*args) == SHAPE, at
