@@ -547,8 +547,8 @@ PA_API int pa_decode_attention_fp8_scaled(const void* q, const void* key_cache,
  * V hold (NaN included).
  * A V scale more than 2^24 below the largest of the sequence loses weight
  * precision, as in pa_decode_attention_fp8_scaled.
- * partition_size  tokens per partition of the keys that one tile of 128
- *               (token, query head) rows spans, rounded up to 128; 0 picks one from
+ * partition_size  tokens per partition of the keys that one CTA's (token,
+ *               query head) rows span, rounded up to 128; 0 picks one from
  *               the SM count. Results are reproducible bit for bit for
  *               fixed arguments.
  *

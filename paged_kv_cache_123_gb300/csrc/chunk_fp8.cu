@@ -11,22 +11,28 @@
 // tokens; "PagedAttention 核心创新深度分析" §3.5: the KV spec carries a
 // quantisation mode.)
 //
-// One CTA owns 128 rows, (new token, query head) pairs of one KV head, and
-// walks their keys in tiles of 128 tokens:
+// One CTA owns up to 256 rows, (new token, query head) pairs of one KV head,
+// as two tiles of 128 (the MMA's M), and walks their keys in tiles of 128
+// tokens. Two chains, each with its scores, its output in tensor memory and
+// four softmax warps, keep the tensor core busy: while one chain's softmax
+// runs, the core works for the other. With more than 128 rows each chain has
+// its row tile and takes every key tile (a key tile is loaded and widened
+// once for 256 rows); with fewer, both have the same rows and take the key
+// tiles in turn, and their results meet at the end.
 //   * a producer warp brings the tiles' codes (K and V in the order in which
 //     the MMAs need them) by 3-D TMA boxes, one per block piece, into a ring
-//     of four raw stages;
+//     of raw stages;
 //   * four converter warps widen each raw tile to fp16 (E4M3 is exact in
 //     fp16) into the 128-byte-swizzled operand layout of the MMA, two stages
 //     each of K and V, and clear rows without a token on the way. They also
-//     build the Q tile: fp16 with each row divided by a power of two, so
+//     build the Q tiles: fp16 with each row divided by a power of two, so
 //     that a bf16 query keeps its 8 significant bits down to 2^-24 of the
 //     row's largest value;
-//   * one thread issues S = Q K^T into one of two TMEM score buffers and
-//     O += P V with P (fp16, over the scores) read from TMEM;
-//   * eight softmax warps, half a row per thread, keep the running maximum
-//     and the sum in fp32 registers; the output in TMEM is rescaled only
-//     when a row's maximum grew by more than 2^8.
+//   * one thread issues S = Q K^T into the chain's TMEM scores and O += P V
+//     with P (fp16, over the scores) read from TMEM;
+//   * a softmax thread owns one row: scores in registers, running maximum
+//     and sum in fp32; the output in TMEM is rescaled only when the maximum
+//     grew by more than 2^8.
 // fp16 products for both query types: weights are rounded to 11 bits, one
 // rounding, in [0, 2^8].
 //
@@ -56,26 +62,28 @@
 namespace pa {
 namespace {
 
-constexpr int kRows = 128;                // query rows per CTA (MMA M)
+constexpr int kRows = 128;                // rows of a chain (MMA M)
 constexpr int kKv = 128;                  // KV tokens per tile
-constexpr int kRaw = 4;                   // raw stages
-constexpr int kSoftmaxWarps = 8;
-constexpr int kProducerWarp = 8;
-constexpr int kMmaWarp = 9;
-constexpr int kConvWarp = 10;             // first of four
+constexpr int kMmaWarp = 0;
+constexpr int kProducerWarp = 1;
+constexpr int kConvWarp = 4;              // 4-7: converters
 constexpr int kConvWarps = 4;
-constexpr int kThreads = (kConvWarp + kConvWarps) * 32;
-constexpr int kCols = kKv / 2;            // score columns per softmax thread
-constexpr uint32_t kTmemCols = 512;       // S0 [0,128), S1 [128,256), O [256,256+D)
+constexpr int kSoftmaxWarp = 8;           // 8-11, 12-15: the chains' softmax
+constexpr int kThreads = 512;
+constexpr int kHalf = kKv / 2;            // tokens of a softmax step
+constexpr int kMaxRaw = 4;                // raw stages with one row tile; 2 with two
+constexpr uint32_t kTmemCols = 512;       // scores: chain c at 128 c; outputs: 256 + 128 c
 constexpr uint32_t kOCol = 256;
 constexpr long long kWaitCycles = 4000000000LL;
 constexpr float kLazyLog2 = 8.f;
 #define kNegInfC (-__int_as_float(0x7f800000))
 
+// barriers; kSFull has one per chain, kPFull and kODone one per chain and half
+// (2 c + h), each with one phase per tile of the chain
 enum : int {
-  kRawFull = 0, kRawEmpty = kRaw, kKFull = 2 * kRaw, kKEmpty = kKFull + 2, kVFull = kKEmpty + 2,
-  kVEmpty = kVFull + 2, kSFull = kVEmpty + 2, kPFull = kSFull + 2, kODone, kDone, kQFull, kConvDone,
-  kBars
+  kRawFull = 0, kRawEmpty = kMaxRaw, kKFull = 2 * kMaxRaw, kKEmpty = kKFull + 2,
+  kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2, kPFull = kSFull + 2,
+  kODone = kPFull + 4, kDone = kODone + 4, kQFull, kConvDone, kBars
 };
 
 template <int D>
@@ -84,8 +92,9 @@ struct ChunkLayout {
   // the limit of 227 KB for head size 128
   static constexpr int BAR_OFF = 0;
   static constexpr int MISC_OFF = (kBars * 8 + 15) / 16 * 16;   // tmem base, abort, masks, NaN
-  static constexpr int XCH_OFF = MISC_OFF + 32;                 // float [2][2][128]
-  static constexpr int SMALL = XCH_OFF + 2 * 2 * kRows * 4;
+  static constexpr int ROW_OFF = MISC_OFF + 32;                 // float [2][128] Q row factors
+  static constexpr int ML_OFF = ROW_OFF + 2 * kRows * 4;        // float [2][128] second chain's m, l
+  static constexpr int SMALL = ML_OFF + 2 * kRows * 4;
   static constexpr int HALVES = D / 64;
   static constexpr int HALF = kKv * 128;                        // 128 rows x 64 fp16
   static constexpr int TILE = HALVES * HALF;
@@ -93,9 +102,12 @@ struct ChunkLayout {
   static constexpr int Q_OFF = 0;                               // from the aligned base
   static constexpr int K_OFF = TILE;
   static constexpr int V_OFF = K_OFF + 2 * TILE;
-  static constexpr int RAW_OFF = V_OFF + 2 * TILE;
-  static constexpr int TILES = RAW_OFF + kRaw * RAW;
+  static constexpr int RAW_OFF = V_OFF + 2 * TILE;              // two raw stages, then
+  static constexpr int Q2_OFF = RAW_OFF + 2 * RAW;              // Q tile 2 or two more
+  static constexpr int TILES = Q2_OFF + TILE;
   static constexpr int SMEM = 3 * 1024 + TILES;
+  static_assert(2 * RAW <= TILE, "two raw stages where Q tile 2 is");
+  static_assert(kRows * D * 4 <= 2 * TILE, "the second chain's output where K is");
   static_assert(SMALL <= 3 * 1024 - 16, "small region");
   static_assert(SMEM <= 232448, "over the shared memory of one CTA");
 };
@@ -149,16 +161,6 @@ __device__ __forceinline__ uint32_t pack_out<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
-// Barrier 1 over the softmax warps that also returns whether all passed `ok`.
-__device__ __forceinline__ bool softmax_all(bool ok) {
-  uint32_t out;
-  asm volatile(
-      "{\n .reg .pred pi, po;\n setp.ne.u32 pi, %1, 0;\n"
-      " barrier.cta.red.and.pred po, 1, 256, pi;\n selp.u32 %0, 1, 0, po;\n}\n"
-      : "=r"(out) : "r"((uint32_t)ok) : "memory");
-  return out != 0;
-}
-
 // What a row tile covers: tokens i_first .. i_last of the sequence's new
 // ones, keys kv_base (a multiple of the tile) .. kv_all - 1, of which those
 // before kv_first are in no row's window; `count` partitions.
@@ -167,9 +169,9 @@ struct TileSpan {
 };
 __device__ __forceinline__ TileSpan tile_span(const ChunkArgs& a, int G, int n, int L, int qt) {
   TileSpan t;
-  const int r0 = qt * kRows;
+  const int r0 = qt * a.rows_per_cta;
   t.i_first = r0 / G;
-  t.i_last = min(n - 1, (r0 + kRows - 1) / G);
+  t.i_last = min(n - 1, (r0 + a.rows_per_cta - 1) / G);
   t.kv_all = L - n + t.i_last + 1;
   const int p0 = L - n + t.i_first;
   t.kv_first = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
@@ -213,13 +215,14 @@ struct Pieces {
 template <int D>
 __device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtensorMap* tmV,
                         const Pieces& pc, int kvh, uint32_t tiles, uint32_t bar,
-                        volatile uint32_t* masks, volatile int* abort_flag, int lane) {
+                        volatile uint32_t* masks, volatile int* abort_flag, int raw_log2,
+                        int lane) {
   using Ly = ChunkLayout<D>;
   if (lane == 0) {
     prefetch_tensormap(tmK);
     prefetch_tensormap(tmV);
   }
-  const int n = pc.ntiles;
+  const int n = pc.ntiles, nraw = 1 << raw_log2;
   // entries of the K tile to come and of the one behind it are read ahead;
   // the two K tiles gone by are kept for their V
   int e0 = pc.entry(0, lane), e1 = pc.entry(1, lane), h0 = -1, h1 = -1;
@@ -244,12 +247,12 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtens
         tok + pc.R > pc.kv_first)
       latch(a.err, PA_ERR_OUT_OF_RANGE);
     const unsigned pm = __ballot_sync(0xffffffffu, mine);
-    const int st = it % kRaw;
+    const int st = it & (nraw - 1);
     int ok = 1;
     if (lane == 0) {
-      if (it >= kRaw)
-        ok = mbar_wait_bounded(bar + 8u * (kRawEmpty + st), ((it / kRaw) - 1) & 1, abort_flag,
-                               kWaitCycles);
+      if (it >= nraw)
+        ok = mbar_wait_bounded(bar + 8u * (kRawEmpty + st), ((it >> raw_log2) - 1) & 1,
+                               abort_flag, kWaitCycles);
       if (ok) {
         masks[st] = pm;
         mbar_arrive_expect_tx(bar + 8u * (kRawFull + st),
@@ -266,8 +269,8 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtens
   }
   // this warp's copies land before the CTA can leave, also after a timeout
   if (lane == 0)
-    for (int i = issued > kRaw ? issued - kRaw : 0; i < issued; ++i)
-      mbar_wait_drain(bar + 8u * (kRawFull + i % kRaw), (i / kRaw) & 1, kWaitCycles);
+    for (int i = issued > nraw ? issued - nraw : 0; i < issued; ++i)
+      mbar_wait_drain(bar + 8u * (kRawFull + (i & (nraw - 1))), (i >> raw_log2) & 1, kWaitCycles);
 }
 
 // Q row r of the tile to fp16, divided by the power of two of its largest
@@ -318,109 +321,182 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// Raw tile -> fp16 operand tile: token row r, codes 16c .. 16c+15 become two
-// 16-byte chunks of the row's 128-byte line(s), at the swizzled places. Rows
-// without a token become zero. CLEAN: NaN codes become zero; returns whether
-// there were any.
+// A converter lane's place: in each step the four warps take 16 token rows,
+// 16 codes per lane. Codes 16c .. 16c+15 of row r become the 16-byte chunks
+// 2c and 2c + 1 of the row's 64-element line (c / 4), stored at chunk ^ (r &
+// 7); steps are 16 rows apart, so the places only move by whole lines. With
+// head size 128, eight consecutive lanes take the first half of one row and
+// the second half of the next: their 16-byte loads and their stores then hit
+// eight different bank groups.
 template <int D>
-__device__ __forceinline__ bool convert_tile(uint32_t raw, uint32_t dst, bool whole, int rows,
-                                             unsigned pm, int rshift, bool clean, int cw,
-                                             int lane) {
+struct ConvLane {
   using Ly = ChunkLayout<D>;
-  constexpr int UNITS = D / 16;                     // 16-code units per row
-  constexpr int RPW = 32 / UNITS;                   // rows per warp and step
-  constexpr int STEPS = kKv / (RPW * kConvWarps);
-  const int c = lane % UNITS;
+  static constexpr int UNITS = D / 16;
+  static constexpr int ROWS = 32 / UNITS * kConvWarps;   // rows per step
+  static constexpr int STEPS = kKv / ROWS;
+  int row;                     // row in step 0
+  uint32_t src, dst0, dst1;    // byte offsets in the raw and the fp16 tile
+  __device__ __forceinline__ ConvLane(int cw, int lane) {
+    int c;
+    if (D == 128) {
+      const int b = (lane >> 2) & 1, q = lane >> 3;
+      row = cw * 4 + 2 * (q >> 1) + b;
+      c = (lane & 3) + 4 * (b ^ (q & 1));
+    } else {
+      row = cw * 8 + (lane >> 2);
+      c = lane & 3;
+    }
+    src = row * D + c * 16;
+    const int k = (2 * c) & 7;
+    const uint32_t line = (c >> 2) * Ly::HALF + row * 128;
+    dst0 = line + ((k ^ (row & 7)) << 4);
+    dst1 = line + (((k + 1) ^ (row & 7)) << 4);
+  }
+};
+static_assert(ConvLane<128>::ROWS % 8 == 0 && ConvLane<64>::ROWS % 8 == 0, "swizzle period");
+
+// Raw tile -> fp16 operand tile. Rows without a token become zero. clean:
+// NaN codes become zero; returns whether this lane met any.
+template <int D>
+__device__ __forceinline__ bool convert_tile(const ConvLane<D>& ln, uint32_t raw, uint32_t dst,
+                                             bool whole, int rows, unsigned pm, int rshift,
+                                             bool clean) {
+  using CL = ConvLane<D>;
   bool seen = false;
-#pragma unroll 4
-  for (int s = 0; s < STEPS; ++s) {
-    const int r = (s * kConvWarps + cw) * RPW + lane / UNITS;
-    uint32_t w[4];
+  // all loads first: their latency is paid once
+  uint32_t w[CL::STEPS][4];
+#pragma unroll
+  for (int s = 0; s < CL::STEPS; ++s)
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(raw + r * D + c * 16) : "memory");
-    if (!whole && !(r < rows && ((pm >> (r >> rshift)) & 1u))) w[0] = w[1] = w[2] = w[3] = 0u;
-    if (clean) {
+                 : "=r"(w[s][0]), "=r"(w[s][1]), "=r"(w[s][2]), "=r"(w[s][3])
+                 : "r"(raw + ln.src + s * CL::ROWS * D));
+  if (!whole) {
+#pragma unroll
+    for (int s = 0; s < CL::STEPS; ++s) {
+      const int r = ln.row + s * CL::ROWS;
+      if (!(r < rows && ((pm >> (r >> rshift)) & 1u))) w[s][0] = w[s][1] = w[s][2] = w[s][3] = 0u;
+    }
+  }
+  if (clean) {
+#pragma unroll
+    for (int s = 0; s < CL::STEPS; ++s)
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint32_t nb = nan_bytes(w[k]);
+        const uint32_t nb = nan_bytes(w[s][k]);
         if (nb != 0u) {
           seen = true;
-          w[k] &= ~((nb >> 7) * 0xffu);
+          w[s][k] &= ~((nb >> 7) * 0xffu);
         }
       }
-    }
+  }
+#pragma unroll
+  for (int s = 0; s < CL::STEPS; ++s) {
     uint32_t h[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[k], h[2 * k], h[2 * k + 1]);
-    const uint32_t line = dst + (D == 128 ? (c >> 2) * Ly::HALF : 0) + r * 128;
-    const int k0 = (2 * c) & 7;
-    // the eight lanes of a store phase cover two half lines: the second half
-    // stores its odd chunk first, so that they hit different banks
-    const bool swap = D == 128 && c >= 4;
-    const uint32_t d0 = line + ((k0 ^ (r & 7)) << 4), d1 = line + (((k0 + 1) ^ (r & 7)) << 4);
-    const uint32_t da = swap ? d1 : d0, db = swap ? d0 : d1;
+    for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[s][k], h[2 * k], h[2 * k + 1]);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(da), "r"(swap ? h[4] : h[0]), "r"(swap ? h[5] : h[1]),
-                   "r"(swap ? h[6] : h[2]), "r"(swap ? h[7] : h[3]) : "memory");
+                 ::"r"(dst + ln.dst0 + s * CL::ROWS * 128), "r"(h[0]), "r"(h[1]), "r"(h[2]),
+                   "r"(h[3]) : "memory");
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(db), "r"(swap ? h[0] : h[4]), "r"(swap ? h[1] : h[5]),
-                   "r"(swap ? h[2] : h[6]), "r"(swap ? h[3] : h[7]) : "memory");
+                 ::"r"(dst + ln.dst1 + s * CL::ROWS * 128), "r"(h[4]), "r"(h[5]), "r"(h[6]),
+                   "r"(h[7]) : "memory");
   }
   return seen;
 }
 
-// MMA issue (one thread).
+// MMA issue (the MMA warp, converged; its elected lane issues). The whole of
+// tensor memory is allocated, so its base is 0. `alt`: the chains take the key tiles in turn (the
+// same Q tile); otherwise each takes every tile with its own Q tile. P comes
+// in two halves of 64 tokens. A
+// chain's weights lie over its scores, so its next scores are issued when its
+// last P V has completed; the other chain's softmax runs meanwhile.
 template <int D>
-__device__ void issue(int ntiles, uint32_t tiles, uint32_t bar, uint32_t tmem,
+__device__ void issue(int ntiles, bool alt, uint32_t tiles, uint32_t bar,
                       volatile int* abort_flag) {
   using Ly = ChunkLayout<D>;
   constexpr uint32_t idS = idesc_f16(false, kRows, kKv, false, false);
   constexpr uint32_t idO = idesc_f16(false, kRows, D, false, true);
-  auto issue_s = [&](int t) -> bool {
-    const int sb = t & 1;
-    if (!mbar_wait_bounded(bar + 8u * (kKFull + sb), (t >> 1) & 1, abort_flag, kWaitCycles))
-      return false;
+  // descriptors of the first operands; the others differ by whole 16-byte
+  // units in the address field (no carry: it counts the 227 KB of a CTA)
+  const uint64_t q_desc = smem_desc_sw128(tiles + Ly::Q_OFF, 16, 1024);
+  const uint64_t k_desc = smem_desc_sw128(tiles + Ly::K_OFF, 16, 1024);
+  const uint64_t v_desc = smem_desc_sw128(tiles + Ly::V_OFF, Ly::HALF, 1024);
+  const uint32_t leader = elect_one();
+  auto wait = [&](int b, int parity) {
+    return __all_sync(0xffffffffu, mbar_wait_bounded(bar + 8u * b, parity & 1, abort_flag,
+                                                     kWaitCycles));
+  };
+  auto issue_s = [&](int c, int j) {              // chain c, tile j
     tc_fence_after();
-    const uint32_t qa = tiles + Ly::Q_OFF, kb = tiles + Ly::K_OFF + sb * Ly::TILE;
+    const uint64_t qd = q_desc + (c == 1 && !alt ? (Ly::Q2_OFF - Ly::Q_OFF) >> 4 : 0);
+    const uint64_t kd = k_desc + (uint32_t)(j & 1) * (Ly::TILE >> 4);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-      const uint64_t ad = smem_desc_sw128(qa + (ks >> 2) * Ly::HALF + (ks & 3) * 32, 16, 1024);
-      const uint64_t bd = smem_desc_sw128(kb + (ks >> 2) * Ly::HALF + (ks & 3) * 32, 16, 1024);
-      mma_f16_ss(tmem + sb * kKv, ad, bd, idS, ks > 0 ? 1u : 0u);
+      constexpr int step = Ly::HALF >> 4;
+      mma_f16_ss_if(leader, c * kKv, qd + (ks >> 2) * step + (ks & 3) * 2,
+                    kd + (ks >> 2) * step + (ks & 3) * 2, idS, ks > 0 ? 1u : 0u);
     }
-    mma_commit(bar + 8u * (kSFull + sb));
-    mma_commit(bar + 8u * (kKEmpty + sb));
-    return true;
+    mma_commit_if(leader, bar + 8u * (kSFull + c));
+    if (alt || c == 1) mma_commit_if(leader, bar + 8u * (kKEmpty + (j & 1)));
   };
-  auto issue_pv = [&](int t) -> bool {
-    const int vs = t & 1;
-    if (!mbar_wait_bounded(bar + 8u * kPFull, t & 1, abort_flag, kWaitCycles)) return false;
-    if (!mbar_wait_bounded(bar + 8u * (kVFull + vs), (t >> 1) & 1, abort_flag, kWaitCycles))
-      return false;
+  auto issue_pv = [&](int c, int j, int h, bool first) {
     tc_fence_after();
-    const uint32_t vb = tiles + Ly::V_OFF + vs * Ly::TILE;
-    const uint32_t pt = tmem + (uint32_t)(t & 1) * kKv;
+    const uint64_t vd = v_desc + (uint32_t)(j & 1) * (Ly::TILE >> 4) + h * (kHalf * 128 >> 4);
+    const uint32_t p = c * kKv + h * kHalf;
 #pragma unroll
-    for (int ks = 0; ks < kKv / 16; ++ks) {
-      const uint64_t bd = smem_desc_sw128(vb + ks * 2048, Ly::HALF, 1024);
-      mma_f16_ts(tmem + kOCol, pt + (ks >> 2) * kCols + (ks & 3) * 8, bd, idO,
-                 (t > 0 || ks > 0) ? 1u : 0u);
-    }
-    mma_commit(bar + 8u * kODone);
-    mma_commit(bar + 8u * (kVEmpty + vs));
-    return true;
+    for (int ks = 0; ks < kHalf / 16; ++ks)
+      mma_f16_ts_if(leader, kOCol + c * kKv, p + ks * 8, vd + ks * (2048 >> 4), idO,
+                    (!first || ks > 0) ? 1u : 0u);
+    mma_commit_if(leader, bar + 8u * (kODone + 2 * c + h));
+    if (h == 1 && (alt || c == 1)) mma_commit_if(leader, bar + 8u * (kVEmpty + (j & 1)));
   };
-  bool ok = mbar_wait_bounded(bar + 8u * kQFull, 0, abort_flag, kWaitCycles);
-  for (int t = 0; ok && t < 2 && t < ntiles; ++t) ok = issue_s(t);
-  for (int j = 0; ok && j < ntiles; ++j) {
-    ok = issue_pv(j);
-    if (ok && j + 2 < ntiles) {
-      ok = mbar_wait_bounded(bar + 8u * kODone, j & 1, abort_flag, kWaitCycles);
-      if (ok) ok = issue_s(j + 2);
+  bool ok = wait(kQFull, 0);
+  if (alt) {
+    for (int j = 0; ok && j < 2 && j < ntiles; ++j) {
+      ok = wait(kKFull + j, 0);
+      if (ok) issue_s(j, j);
+    }
+    for (int j = 0; ok && j < ntiles; ++j) {
+      const int c = j & 1, t = j >> 1;
+      ok = wait(kVFull + c, t) && wait(kPFull + 2 * c, t);
+      if (!ok) break;
+      issue_pv(c, j, 0, t == 0);
+      ok = wait(kPFull + 2 * c + 1, t);
+      if (!ok) break;
+      issue_pv(c, j, 1, false);
+      if (j + 2 < ntiles) {
+        ok = wait(kKFull + c, t + 1) && wait(kODone + 2 * c + 1, t);
+        if (ok) issue_s(c, j + 2);
+      }
+    }
+  } else {
+    ok = ok && wait(kKFull, 0);
+    if (ok) {
+      issue_s(0, 0);
+      issue_s(1, 0);
+    }
+    for (int j = 0; ok && j < ntiles; ++j) {
+      const bool more = j + 1 < ntiles;
+      ok = wait(kVFull + (j & 1), j >> 1);
+      if (ok && more) ok = wait(kKFull + ((j + 1) & 1), (j + 1) >> 1);
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (ok) ok = wait(kPFull + 2 * c, j);
+        if (!ok) break;
+        issue_pv(c, j, 0, j == 0);
+        ok = wait(kPFull + 2 * c + 1, j);
+        if (!ok) break;
+        issue_pv(c, j, 1, false);
+        if (more) {
+          ok = wait(kODone + 2 * c + 1, j);
+          if (ok) issue_s(c, j + 1);
+        }
+      }
     }
   }
-  mma_commit(bar + 8u * kDone);
+  // every MMA issued above has completed once this barrier fires (waited
+  // for also after a timeout, before the CTA frees its TMEM)
+  mma_commit_if(leader, bar + 8u * kDone);
   mbar_wait_drain(bar + 8u * kDone, 0, kWaitCycles);
 }
 
@@ -436,14 +512,16 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem_raw + Ly::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + Ly::MISC_OFF + 4);
   volatile uint32_t* masks = misc + 2;
-  float* xch = reinterpret_cast<float*>(smem_raw + Ly::XCH_OFF);   // [2][2 halves][128]
+  float* row_factor = reinterpret_cast<float*>(smem_raw + Ly::ROW_OFF);   // [2][128]
+  float* second_ml = reinterpret_cast<float*>(smem_raw + Ly::ML_OFF);     // [2][128]
   if (tiles + Ly::TILES > sbase + Ly::SMEM) {       // base too far off 1024 bytes
     if (threadIdx.x == 0) latch(a.err, PA_ERR_CUDA);
     return;
   }
 
   const int s = blockIdx.z, kvh = blockIdx.y;
-  const int row_tiles = (int)(((int64_t)a.max_query_len * G + kRows - 1) / kRows);
+  const int row_tiles =
+      (int)(((int64_t)a.max_query_len * G + a.rows_per_cta - 1) / a.rows_per_cta);
   const int qt = row_tiles - 1 - (int)(blockIdx.x % row_tiles);    // longest rows first
   const int split = (int)(blockIdx.x / row_tiles);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -454,16 +532,18 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) latch(a.err, PA_ERR_OUT_OF_RANGE);
     return;
   }
-  const int r0 = qt * kRows;
+  const int r0 = qt * a.rows_per_cta;
   if (r0 >= n * G) return;
   const TileSpan sp = tile_span(a, G, n, L, qt);
   const int kv_lo = sp.kv_base + split * a.partition;
   if (split >= sp.count) return;
   const int kv_end = min(sp.kv_all, kv_lo + a.partition);
   const int ntiles = (kv_end - kv_lo + kKv - 1) / kKv;
+  const bool alt = n * G - r0 <= kRows;             // one row tile: key tiles in turn
+  const int raw_log2 = alt ? 2 : 1, nraw = 1 << raw_log2;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kRaw; ++i) {
+    for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(bar + 8u * (kRawFull + i), 1);
       mbar_init(bar + 8u * (kRawEmpty + i), kConvWarps);
     }
@@ -474,8 +554,10 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       mbar_init(bar + 8u * (kVEmpty + i), 1);
       mbar_init(bar + 8u * (kSFull + i), 1);
     }
-    mbar_init(bar + 8u * kPFull, kSoftmaxWarps);
-    mbar_init(bar + 8u * kODone, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar + 8u * (kPFull + i), 4);
+      mbar_init(bar + 8u * (kODone + i), 1);
+    }
     mbar_init(bar + 8u * kDone, 1);
     mbar_init(bar + 8u * kQFull, kConvWarps);
     mbar_init(bar + 8u * kConvDone, kConvWarps);
@@ -509,71 +591,79 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   const int pos_first = L - n + sp.i_first;
   const int lo_last = a.window > 0 ? max(0, L - n + sp.i_last + 1 - a.window) : 0;
 
-  if (warp == kProducerWarp) {
-    produce<D>(a, &tmK, &tmV, pc, kvh, tiles, bar, masks, abort_flag, lane);
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) issue<D>(ntiles, tiles, bar, tmem, abort_flag);
-    __syncwarp();
-  } else if (warp >= kConvWarp) {
-    const int cw = warp - kConvWarp;
-    {
-      const int r = cw * 32 + lane, rr = r0 + r;
-      const int i = rr / G;
-      const bool live = i < n;
-      const T* src = reinterpret_cast<const T*>(a.q) +
-                     ((int64_t)(q0 + (live ? i : 0)) * a.num_q_heads + (int64_t)kvh * G + rr % G) * D;
-      // the factors sit where the second exchange buffer will be: it is
-      // first written after every softmax thread has read its factor
-      xch[2 * kRows + r] = convert_q_row<T, D>(src, live, a.scale, tiles + Ly::Q_OFF, r);
+  if (warp < kSoftmaxWarp) {
+    if (warp == kProducerWarp) {
+      produce<D>(a, &tmK, &tmV, pc, kvh, tiles, bar, masks, abort_flag, raw_log2, lane);
+    } else if (warp == kMmaWarp) {
+      if (tmem == 0) issue<D>(ntiles, alt, tiles, bar, abort_flag);
+      else *abort_flag = 1;
+      __syncwarp();
+    } else if (warp >= kConvWarp) {
+      const int cw = warp - kConvWarp;
+      const ConvLane<D> ln(cw, lane);
+      for (int c = 0; c < (alt ? 1 : 2); ++c) {
+        const int r = cw * 32 + lane, rr = r0 + c * kRows + r;
+        const int i = rr / G;
+        const bool live = i < n;
+        const T* src =
+            reinterpret_cast<const T*>(a.q) +
+            ((int64_t)(q0 + (live ? i : 0)) * a.num_q_heads + (int64_t)kvh * G + rr % G) * D;
+        row_factor[c * kRows + r] = convert_q_row<T, D>(
+            src, live, a.scale, tiles + (c == 0 ? Ly::Q_OFF : Ly::Q2_OFF), r);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar + 8u * kQFull);
-    }
-    for (int it = 0; it < 2 * ntiles; ++it) {
-      int j;
-      const bool isv = item_of(it, ntiles, &j);
-      const int rs = it % kRaw, st = j & 1;
-      bool ok = mbar_wait_bounded(bar + 8u * (kRawFull + rs), (it / kRaw) & 1, abort_flag,
-                                  kWaitCycles);
-      if (ok && j >= 2)
-        ok = mbar_wait_bounded(bar + 8u * ((isv ? kVEmpty : kKEmpty) + st), ((j >> 1) - 1) & 1,
-                               abort_flag, kWaitCycles);
-      if (!__all_sync(0xffffffffu, ok)) break;
-      const int ts = kv_lo + j * kKv;
-      const int rows = min(kKv, kv_end - ts);
-      const unsigned pm = masks[rs];
-      const bool clean = isv && (ts + kKv - 1 > pos_first || ts < lo_last);
-      const bool seen = convert_tile<D>(
-          tiles + Ly::RAW_OFF + rs * Ly::RAW,
-          tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE, pm == full_mask && rows == kKv,
-          rows, pm, rshift, clean, cw, lane);
-      if (seen) misc[6] = 1;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(bar + 8u * (kRawEmpty + rs));
-        mbar_arrive(bar + 8u * ((isv ? kVFull : kKFull) + st));
+      for (int it = 0; it < 2 * ntiles; ++it) {
+        int j;
+        const bool isv = item_of(it, ntiles, &j);
+        const int rs = it & (nraw - 1), st = j & 1;
+        bool ok = mbar_wait_bounded(bar + 8u * (kRawFull + rs), (it >> raw_log2) & 1, abort_flag,
+                                    kWaitCycles);
+        if (ok && j >= 2)
+          ok = mbar_wait_bounded(bar + 8u * ((isv ? kVEmpty : kKEmpty) + st), ((j >> 1) - 1) & 1,
+                                 abort_flag, kWaitCycles);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const int ts = kv_lo + j * kKv;
+        const int rows = min(kKv, kv_end - ts);
+        const unsigned pm = masks[rs];
+        const bool clean = isv && (ts + kKv - 1 > pos_first || ts < lo_last);
+        const bool seen = convert_tile<D>(
+            ln, tiles + Ly::RAW_OFF + rs * Ly::RAW,
+            tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE,
+            pm == full_mask && rows == kKv, rows, pm, rshift, clean);
+        if (seen) misc[6] = 1;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar + 8u * (kRawEmpty + rs));
+          mbar_arrive(bar + 8u * ((isv ? kVFull : kKFull) + st));
+        }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar + 8u * kConvDone);
     }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar + 8u * kConvDone);
   } else {
-    // ---- softmax: thread = (half hf, row r)
-    const int hf = warp >> 2;
+    // ---- softmax of chain c: thread = row r of its tile
+    const int c = (warp - kSoftmaxWarp) >> 2;
     const int r = (warp & 3) * 32 + lane;
-    const int rr = r0 + r;
+    const int rr = r0 + (alt ? 0 : c * kRows) + r;
     const int i = rr / G;
     const bool rv = i < n;
     const int pos = rv ? L - n + i : -1;
     const int lo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
     const bool idle = __all_sync(0xffffffffu, !rv);   // no row here holds a token
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t sadr = tmem + lanes + c * kKv;
+    const uint32_t oadr = tmem + lanes + kOCol + c * kKv;
     bool ok = mbar_wait_bounded(bar + 8u * kQFull, 0, abort_flag, kWaitCycles);
     // logit factor in the log2 domain (Q carries the scale's sign and zero)
     const float f0 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e *
-                     (SCALED ? 1.f : a.k_scale) * xch[2 * kRows + r];
+                     (SCALED ? 1.f : a.k_scale) * row_factor[(alt ? 0 : c * kRows) + r];
 
-    int ent = pc.entry(0, lane), ent_next = pc.entry(1, lane);
+    // this chain's tiles: j = j0, j0 + dj, ...
+    const int j0 = alt ? c : 0, dj = alt ? 2 : 1;
+    int ent = pc.entry(j0, lane), ent_next = pc.entry(j0 + dj, lane);
     float ksl = 1.f, vsl = 0.f;                       // scales of this lane's piece
     auto load_scales = [&](int e, float& k, float& v) {
       k = 1.f;
@@ -585,56 +675,24 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     };
     load_scales(ent, ksl, vsl);
     float m_use = kNegInfC, l = 0.f, vref = 0.f;
-    for (int j = 0; j < ntiles; ++j) {
-      const int sb = j & 1;
+    int t = 0;
+    for (int j = j0; j < ntiles; j += dj, ++t) {
       const int ts = kv_lo + j * kKv;
       const int te = min(kv_end, ts + kKv);
       const unsigned pm = __ballot_sync(0xffffffffu, ent >= 0 && ent < a.num_blocks);
       float ks_next, vs_next;
       load_scales(ent_next, ks_next, vs_next);
-      const int ent_2 = pc.entry(j + 2, lane);
+      const int ent_2 = pc.entry(j + 2 * dj, lane);
       if (ok)
-        ok = mbar_wait_bounded(bar + 8u * (kSFull + sb), (j >> 1) & 1, abort_flag, kWaitCycles);
+        ok = mbar_wait_bounded(bar + 8u * (kSFull + c), t & 1, abort_flag, kWaitCycles);
       ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
       tc_fence_after();
       const bool whole = pm == full_mask && te - ts == kKv;
-      const int hi = min(pos, te - 1) - ts - hf * kCols;     // last own column in sight
-      const int first = lo - ts - hf * kCols;                // first own column in sight
-      const bool fast = __all_sync(0xffffffffu, (whole && hi >= kCols - 1 && first <= 0) || !rv);
-      const uint32_t sadr = tmem + lanes + sb * kKv + hf * kCols;
-      uint32_t v[kCols];
-      if (ok && !idle) {
-        tmem_ld64(sadr, v);
-      } else {
-#pragma unroll
-        for (int e = 0; e < kCols; ++e) v[e] = 0u;
-      }
-      if (!fast && rv) {
-        // what a row does not see becomes -inf in place: weight 0 below
-#pragma unroll
-        for (int ch = 0; ch < kCols / 32; ++ch) {
-          const int c0 = ch * 32;
-          uint32_t m = hi < c0 ? 0u : hi >= c0 + 31 ? 0xffffffffu : (2u << (hi - c0)) - 1u;
-          if (first > c0) m &= first > c0 + 31 ? 0u : 0xffffffffu << (first - c0);
-          if (!whole) {
-            const int g0 = hf * kCols + c0;
-            uint32_t p = 0;
-            if (pc.R >= 32) {
-              p = ((pm >> (g0 >> rshift)) & 1u) ? 0xffffffffu : 0u;
-            } else {
-              for (int k = 0; k < 32 / pc.R; ++k)
-                if ((pm >> ((g0 >> rshift) + k)) & 1u) p |= ((1u << pc.R) - 1u) << (k * pc.R);
-            }
-            m &= p;
-          }
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (!((m >> e) & 1u)) v[c0 + e] = __float_as_uint(kNegInfC);
-        }
-      }
-      // the tile's V reference: all warps see the same pieces
-      float alpha_v = 1.f;
-      float rcp_ref = 0.f;
+      const int hi = min(pos, te - 1) - ts;          // last column in sight
+      const int first = lo - ts;                     // first column in sight
+      const bool fast = __all_sync(0xffffffffu, (whole && hi >= kKv - 1 && first <= 0) || !rv);
+      float alpha_v = 1.f, rcp_ref = 0.f;
       if (SCALED) {
         const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vsl)));
         if (top > vref) {
@@ -643,135 +701,196 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         }
         rcp_ref = vref > 0.f ? 1.f / vref : 0.f;
       }
-      // pass 1: the half row's maximum
-      float mx = kNegInfC;
-      if (ok && !idle) {
-        if (!SCALED) {
-          float mx0 = kNegInfC, mx1 = kNegInfC;
+      // the tile in two steps of 64 tokens: the first half's P V runs while
+      // the second half's weights are made
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        if (!idle) {
+          uint32_t v[kHalf];
+          tmem_ld64(sadr + h * kHalf, v);
+          if (!fast && rv) {
+            // what a row does not see becomes -inf in place: weight 0 below
 #pragma unroll
-          for (int e = 0; e < kCols; e += 4) {
-            mx0 = cfmax3(mx0, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
-            mx1 = cfmax3(mx1, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
+            for (int ch = 0; ch < kHalf / 32; ++ch) {
+              const int c0 = h * kHalf + ch * 32;
+              uint32_t m = hi < c0 ? 0u : hi >= c0 + 31 ? 0xffffffffu : (2u << (hi - c0)) - 1u;
+              if (first > c0) m &= first > c0 + 31 ? 0u : 0xffffffffu << (first - c0);
+              if (!whole) {
+                uint32_t p = 0;
+                if (pc.R >= 32) {
+                  p = ((pm >> (c0 >> rshift)) & 1u) ? 0xffffffffu : 0u;
+                } else {
+                  for (int k = 0; k < 32 / pc.R; ++k)
+                    if ((pm >> ((c0 >> rshift) + k)) & 1u) p |= ((1u << pc.R) - 1u) << (k * pc.R);
+                }
+                m &= p;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!((m >> e) & 1u)) v[ch * 32 + e] = __float_as_uint(kNegInfC);
+            }
           }
-          mx = fmaxf(mx0, mx1) * f0;
-        } else {
+          // pass 1: the maximum
+          float mx = kNegInfC;
+          if (!SCALED) {
+            float m4[4] = {kNegInfC, kNegInfC, kNegInfC, kNegInfC};
 #pragma unroll
-          for (int g = 0; g < kCols / 8; ++g) {
-            const float kf = __shfl_sync(0xffffffffu, ksl, (hf * kCols + 8 * g) >> rshift) * f0;
-            float m0 = fmaxf(__uint_as_float(v[8 * g]), __uint_as_float(v[8 * g + 1]));
-            float m1 = fmaxf(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
-            m0 = cfmax3(m0, __uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
-            m1 = cfmax3(m1, __uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
-            mx = fmaxf(mx, fmaxf(m0, m1) * kf);
+            for (int e = 0; e < kHalf; e += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                m4[k] = cfmax3(m4[k], __uint_as_float(v[e + 2 * k]),
+                               __uint_as_float(v[e + 2 * k + 1]));
+            mx = cfmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * f0;
+          } else {
+#pragma unroll
+            for (int g = 0; g < kHalf / 8; ++g) {
+              const float kf =
+                  __shfl_sync(0xffffffffu, ksl, (h * kHalf + 8 * g) >> rshift) * f0;
+              float m0 = fmaxf(__uint_as_float(v[8 * g]), __uint_as_float(v[8 * g + 1]));
+              float m1 = fmaxf(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
+              m0 = cfmax3(m0, __uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
+              m1 = cfmax3(m1, __uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
+              mx = fmaxf(mx, fmaxf(m0, m1) * kf);
+            }
           }
-        }
-      }
-      // the two halves meet; the buffers alternate, so one barrier a tile
-      xch[(sb * 2 + hf) * kRows + r] = mx;
-      ok = softmax_all(ok);
-      if (!ok) break;
-      mx = fmaxf(mx, xch[(sb * 2 + (hf ^ 1)) * kRows + r]);
-      const float m_new = fmaxf(m_use, mx);
-      float alpha = 1.f;
-      if (m_use == kNegInfC) {
-        m_use = m_new;                               // nothing accumulated yet
-      } else if (m_new > m_use + kLazyLog2) {
-        alpha = exp2f(m_use - m_new);
-        m_use = m_new;
-      }
-      // pass 2: P = 2^(x - m_use) in fp16 over this thread's own scores; a
-      // row that has seen nothing has only -inf scores and weights of 0
-      const float nm = m_use == kNegInfC ? 0.f : -m_use;
-      uint64_t sum = pair(0.f, 0.f);
-#pragma unroll
-      for (int ch = 0; ch < kCols / 32; ++ch) {
-        uint32_t pk[16];
-        if (idle) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-        } else {
+          const float m_new = fmaxf(m_use, mx);
+          float alpha = 1.f;
+          if (m_use == kNegInfC) {
+            m_use = m_new;                           // nothing accumulated yet
+          } else if (m_new > m_use + kLazyLog2) {
+            alpha = exp2f(m_use - m_new);
+            m_use = m_new;
+          }
+          // pass 2: P = 2^(x - m_use) in fp16 over this row's own scores; a
+          // row that has seen nothing has only -inf scores and weights of 0
+          const float nm = m_use == kNegInfC ? 0.f : -m_use;
+          uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
           const uint64_t cm = pair(nm, nm);
           uint64_t fm = pair(f0, f0), rm = 0;
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            if (SCALED && (e & 7) == 0) {
-              const int src = (hf * kCols + ch * 32 + e) >> rshift;
-              const float kf = __shfl_sync(0xffffffffu, ksl, src) * f0;
-              const float rt = __shfl_sync(0xffffffffu, vsl, src) * rcp_ref;
-              fm = pair(kf, kf);
-              rm = pair(rt, rt);
-            }
-            float x0, x1;
-            unpair(fma_pair(pair(__uint_as_float(v[ch * 32 + e]),
-                                 __uint_as_float(v[ch * 32 + e + 1])), fm, cm), x0, x1);
-            x0 = cex2(x0);
-            x1 = cex2(x1);
-            uint64_t p = pair(x0, x1);
-            sum = add_pair(sum, p);
-            if (SCALED) unpair(mul_pair(p, rm), x0, x1);
-            pk[e >> 1] = pack_half(x0, x1);
-          }
-        }
-        tmem_st16(sadr + ch * 16, pk);
-      }
-      float s0, s1;
-      unpair(sum, s0, s1);
-      l = l * alpha + (s0 + s1);
-      const float alpha_o = SCALED ? alpha * alpha_v : alpha;
-      if (__any_sync(0xffffffffu, alpha_o != 1.f)) {
-        if (j >= 1) {
-          ok = mbar_wait_bounded(bar + 8u * kODone, (j - 1) & 1, abort_flag, kWaitCycles);
-          ok = __all_sync(0xffffffffu, ok);
-          tc_fence_after();
-          if (ok) {
-#pragma unroll 1
-            for (int ch = 0; ch < D / 64; ++ch) {
-              const uint32_t oadr = tmem + lanes + kOCol + hf * (D / 2) + ch * 32;
-              uint32_t o[32];
-              tmem_ld32(oadr, o);
+          for (int ch = 0; ch < kHalf / 32; ++ch) {
+            uint32_t pk[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_o);
-              tmem_st32(oadr, o);
+            for (int e = 0; e < 32; e += 2) {
+              if (SCALED && (e & 7) == 0) {
+                const int src = (h * kHalf + ch * 32 + e) >> rshift;
+                const float kf = __shfl_sync(0xffffffffu, ksl, src) * f0;
+                const float rt = __shfl_sync(0xffffffffu, vsl, src) * rcp_ref;
+                fm = pair(kf, kf);
+                rm = pair(rt, rt);
+              }
+              float x0, x1;
+              unpair(fma_pair(pair(__uint_as_float(v[ch * 32 + e]),
+                                   __uint_as_float(v[ch * 32 + e + 1])), fm, cm), x0, x1);
+              x0 = cex2(x0);
+              x1 = cex2(x1);
+              const uint64_t p = pair(x0, x1);
+              if (e & 2) sum1 = add_pair(sum1, p); else sum0 = add_pair(sum0, p);
+              if (SCALED) unpair(mul_pair(p, rm), x0, x1);
+              pk[e >> 1] = pack_half(x0, x1);
+            }
+            tmem_st16(sadr + h * kHalf + ch * 16, pk);
+          }
+          float s0, s1;
+          unpair(add_pair(sum0, sum1), s0, s1);
+          l = l * alpha + (s0 + s1);
+          const float alpha_o = SCALED && h == 0 ? alpha * alpha_v : alpha;
+          if (t + h >= 1 && __any_sync(0xffffffffu, alpha_o != 1.f)) {
+            // after the P V of the step before
+            ok = mbar_wait_bounded(bar + 8u * (kODone + 2 * c + (h ^ 1)), (t - 1 + h) & 1,
+                                   abort_flag, kWaitCycles);
+            ok = __all_sync(0xffffffffu, ok);
+            tc_fence_after();
+            if (ok) {
+#pragma unroll 1
+              for (int ch = 0; ch < D / 32; ++ch) {
+                uint32_t o[32];
+                tmem_ld32(oadr + ch * 32, o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha_o);
+                tmem_st32(oadr + ch * 32, o);
+              }
             }
           }
+          tmem_wait_st();
         }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + 8u * (kPFull + 2 * c + h));
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar + 8u * kPFull);
       ent = ent_next;
       ent_next = ent_2;
       ksl = ks_next;
       vsl = vs_next;
     }
-    // the row's sum, over both halves
-    const int xb = (ntiles & 1) * 2;
-    xch[(xb + hf) * kRows + r] = l;
-    ok = softmax_all(ok);
-    l += xch[(xb + (hf ^ 1)) * kRows + r];
     if (ok) ok = mbar_wait_bounded(bar + 8u * kDone, 0, abort_flag, kWaitCycles);
     if (ok) ok = mbar_wait_bounded(bar + 8u * kConvDone, 0, abort_flag, kWaitCycles);
     tc_fence_after();
     ok = __all_sync(0xffffffffu, ok);
-    if (ok) {
-      const int64_t t = q0 + i;
+    const float unit = SCALED ? vref : a.v_scale;
+    // one row tile: the second chain hands its row over (its output where
+    // the K tiles were: 16-byte pieces of a row, spread over the banks)
+    float4* second_o =
+        reinterpret_cast<float4*>(smem_raw + (tiles - sbase) + Ly::K_OFF);
+    constexpr int PIECES = D / 4;
+    if (alt && c == 1) {
+      if (ok && t > 0 && !idle) {
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t o[32];
+          tmem_ld32(oadr + ch * 32, o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            second_o[r * PIECES + ((ch * 8 + k) ^ (r & 7))] =
+                make_float4(__uint_as_float(o[4 * k]) * unit, __uint_as_float(o[4 * k + 1]) * unit,
+                            __uint_as_float(o[4 * k + 2]) * unit,
+                            __uint_as_float(o[4 * k + 3]) * unit);
+        }
+      }
+      second_ml[r] = t > 0 ? m_use : kNegInfC;
+      second_ml[kRows + r] = t > 0 ? l : 0.f;
+    }
+    if (alt) asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (ok && !idle && !(alt && c == 1)) {
+      float w1 = 1.f, w2 = 0.f;                      // the chains' weights
+      if (alt) {
+        const float m2 = second_ml[r], l2 = second_ml[kRows + r];
+        if (!(m2 == kNegInfC && l2 == 0.f)) {
+          const float m = fmaxf(m_use, m2);
+          w1 = m_use == kNegInfC && l == 0.f ? 0.f : exp2f(m_use - m);
+          w2 = exp2f(m2 - m);
+          l = l * w1 + l2 * w2;
+          m_use = m;
+        }
+      }
+      const int64_t tok = q0 + i;
       const int head = kvh * G + rr % G;
       const bool direct = rv && sp.count == 1;
       const bool partial = rv && sp.count > 1;
-      const float unit = SCALED ? vref : a.v_scale;
-      const float mul = direct ? (l != 0.f ? unit / l : 0.f) : unit;
+      const float inv = direct ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+      const float mul1 = unit * w1 * inv, mul2 = w2 * inv;
+      const bool second = alt && ntiles > 1 && w2 != 0.f;
       const bool nans = misc[6] != 0;
       T* out = reinterpret_cast<T*>(a.out);
-      const int64_t slot = (t * a.num_q_heads + head) * a.num_splits + split;
+      const int64_t slot = (tok * a.num_q_heads + head) * a.num_splits + split;
 #pragma unroll 1
-      for (int ch = 0; ch < D / 64; ++ch) {
-        const int c0 = hf * (D / 2) + ch * 32;
+      for (int ch = 0; ch < D / 32; ++ch) {
+        const int c0 = ch * 32;
         uint32_t o[32];
-        tmem_ld32(tmem + lanes + kOCol + c0, o);
+        tmem_ld32(oadr + c0, o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mul);
+        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * mul1);
+        if (second) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 f = second_o[r * PIECES + ((ch * 8 + k) ^ (r & 7))];
+            o[4 * k] = __float_as_uint(fmaf(f.x, mul2, __uint_as_float(o[4 * k])));
+            o[4 * k + 1] = __float_as_uint(fmaf(f.y, mul2, __uint_as_float(o[4 * k + 1])));
+            o[4 * k + 2] = __float_as_uint(fmaf(f.z, mul2, __uint_as_float(o[4 * k + 2])));
+            o[4 * k + 3] = __float_as_uint(fmaf(f.w, mul2, __uint_as_float(o[4 * k + 3])));
+          }
+        }
         if (nans && rv) {
           // columns in which a token that this row sees, in a cleared tile,
           // holds a NaN
@@ -797,7 +916,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             if ((bad >> e) & 1u) o[e] = 0x7fffffffu;
         }
         if (direct) {
-          uint4* op = reinterpret_cast<uint4*>(out + (t * a.num_q_heads + head) * D + c0);
+          uint4* op = reinterpret_cast<uint4*>(out + (tok * a.num_q_heads + head) * D + c0);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint4 w;
@@ -814,7 +933,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             acc[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
       }
-      if (partial && hf == 0) {
+      if (partial) {
         a.ws_ml[2 * slot] = m_use;
         a.ws_ml[2 * slot + 1] = l;
       }
@@ -844,7 +963,7 @@ __global__ void __launch_bounds__(D) chunk_combine_kernel(const ChunkArgs a) {
   if (s < 0 || s >= a.num_seqs) return;
   const int q0 = a.qsl[s], n = a.qsl[s + 1] - q0, L = a.seq_lens[s];
   if (!lengths_ok(a, q0, n, L)) return;
-  const TileSpan sp = tile_span(a, G, n, L, (int)(((t - q0) * G + head % G) / kRows));
+  const TileSpan sp = tile_span(a, G, n, L, (int)(((t - q0) * G + head % G) / a.rows_per_cta));
   if (sp.count <= 1) return;
   const int64_t base = (t * a.num_q_heads + head) * a.num_splits;
   float M = kNegInfC;
@@ -907,7 +1026,8 @@ cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t st) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
   });
   if (attr != cudaSuccess) return attr;
-  const int64_t row_tiles = ((int64_t)a.max_query_len * G + kRows - 1) / kRows;
+  const int64_t row_tiles =
+      ((int64_t)a.max_query_len * G + a.rows_per_cta - 1) / a.rows_per_cta;
   if (row_tiles * a.num_splits > 0x7fffffffll) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(row_tiles * a.num_splits), a.num_kv_heads, a.num_seqs);
   chunk_fp8_kernel<T, D, G, SCALED><<<grid, kThreads, Ly::SMEM, st>>>(a, tk, tv);
@@ -944,23 +1064,31 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Keys a row tile can span (chunk_plan below and the kernel's tile_span).
+// Rows of a CTA: one tile where no sequence has more, two otherwise.
+static int64_t rows_per_cta(int group, int max_query_len) {
+  return (int64_t)max_query_len * group > kRows ? 2 * kRows : kRows;
+}
+
+// Keys a CTA's rows can span (the kernel's tile_span).
 static int64_t span_of(int group, int max_query_len, int max_seq_len, int window) {
   const int64_t len = max_seq_len > 0 ? max_seq_len : 1;
   if (window <= 0) return len;
-  const int64_t toks = std::min<int64_t>(max_query_len, (kRows + group - 1) / group);
+  const int64_t toks =
+      std::min<int64_t>(max_query_len, rows_per_cta(group, max_query_len) / group);
   return std::min<int64_t>(len, (int64_t)window - 1 + toks + kKv - 1);
 }
 
 void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,
-                int window, int partition_size, int sm_count, int* splits, int* tokens) {
+                int window, int partition_size, int sm_count, int* rows, int* splits,
+                int* tokens) {
   const int64_t len = span_of(group, max_query_len, max_seq_len, window);
   auto round_up = [](int64_t x) { return (x + kKv - 1) / kKv * kKv; };
   int64_t P = round_up(len);
+  const int64_t R = rows_per_cta(group, max_query_len);
   if (partition_size > 0) {
     P = std::min(P, round_up(partition_size));
   } else {
-    const int64_t row_tiles = ((int64_t)max_query_len * group + kRows - 1) / kRows;
+    const int64_t row_tiles = ((int64_t)max_query_len * group + R - 1) / R;
     const int64_t ctas = std::max<int64_t>(1, row_tiles * num_kv_heads * num_seqs);
     if (ctas < 4 * (int64_t)sm_count) {
       int64_t best = -1;
@@ -975,6 +1103,7 @@ void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, in
       }
     }
   }
+  *rows = (int)R;
   *tokens = (int)P;
   *splits = (int)((len + P - 1) / P);
 }
