@@ -24,10 +24,10 @@
 //     of raw stages;
 //   * four converter warps widen each raw tile to fp16 (E4M3 is exact in
 //     fp16) into the 128-byte-swizzled operand layout of the MMA, two stages
-//     each of K and V, and clear rows without a token on the way. They also
-//     build the Q tiles: fp16 with each row divided by a power of two, so
-//     that a bf16 query keeps its 8 significant bits down to 2^-24 of the
-//     row's largest value;
+//     each of K and V, and clear rows without a token on the way;
+//   * the Q tiles are fp16 with each row divided by a power of two, so that a
+//     bf16 query keeps its 8 significant bits down to 2^-24 of the row's
+//     largest value;
 //   * one thread issues S = Q K^T into the chain's TMEM scores and O += P V
 //     with P (fp16, over the scores) read from TMEM;
 //   * a softmax thread owns one row: scores in registers, running maximum
@@ -78,11 +78,11 @@ constexpr long long kWaitCycles = 4000000000LL;
 constexpr float kLazyLog2 = 8.f;
 #define kNegInfC (-__int_as_float(0x7f800000))
 
-// barriers; kSFull has one per chain, kPFull and kODone one per chain and half
-// (2 c + h), each with one phase per tile of the chain
+// barriers; kSFull, kPFull and kODone have one per chain and half (2 c + h),
+// each with one phase per tile of the chain
 enum : int {
   kRawFull = 0, kRawEmpty = kMaxRaw, kKFull = 2 * kMaxRaw, kKEmpty = kKFull + 2,
-  kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2, kPFull = kSFull + 2,
+  kVFull = kKEmpty + 2, kVEmpty = kVFull + 2, kSFull = kVEmpty + 2, kPFull = kSFull + 4,
   kODone = kPFull + 4, kDone = kODone + 4, kQFull, kConvDone, kBars
 };
 
@@ -273,47 +273,64 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtens
       mbar_wait_drain(bar + 8u * (kRawFull + (i & (nraw - 1))), (i >> raw_log2) & 1, kWaitCycles);
 }
 
-// Q row r of the tile to fp16, divided by the power of two of its largest
+// Q rows of a tile to fp16, each divided by the power of two of its largest
 // magnitude (bf16 only: fp16 queries are exact as they are); the sign of a
-// negative scale goes into Q, a zero scale makes it zero. Returns the factor
-// taken out.
-template <typename T, int D>
-__device__ __forceinline__ float convert_q_row(const T* src, bool live, float scale,
-                                               uint32_t qbase, int r) {
+// negative scale goes into Q, a zero scale makes it zero. `factor` gets what
+// was taken out of each row. A warp takes rows row0, row0 + 1, ... (a
+// multiple of 8 of them), 16 bytes per lane, so D / 8 lanes share a row; all
+// loads are issued before the first is used.
+template <typename T, int D, int G, int ROWS>
+__device__ __forceinline__ void convert_q_rows(const ChunkArgs& a, int q0, int n, int kvh,
+                                               int tile_row0, int row0, uint32_t qbase,
+                                               float* factor, int lane) {
   using Ly = ChunkLayout<D>;
-  float mul = scale < 0.f ? -1.f : scale == 0.f ? 0.f : 1.f, back = 1.f;
-  if (std::is_same<T, __nv_bfloat16>::value && live) {
-    uint32_t top = 0;
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 u = *reinterpret_cast<const uint4*>(src + 8 * c);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  constexpr int LPR = D / 8;                        // lanes of a row
+  constexpr int RPS = 32 / LPR;                     // rows of a step
+  constexpr int STEPS = ROWS / RPS;
+  const int sub = lane / LPR, c = lane % LPR;
+  uint4 u[STEPS];
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int rr = tile_row0 + row0 + s * RPS + sub;
+    u[s] = make_uint4(0u, 0u, 0u, 0u);
+    if (rr / G < n)
+      u[s] = *reinterpret_cast<const uint4*>(
+          reinterpret_cast<const T*>(a.q) +
+          ((int64_t)(q0 + rr / G) * a.num_q_heads + (int64_t)kvh * G + rr % G) * D + 8 * c);
+  }
+  const float sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    const int r = row0 + s * RPS + sub;
+    float mul = sign, back = 1.f;
+    if (std::is_same<T, __nv_bfloat16>::value) {
+      const uint32_t w[4] = {u[s].x, u[s].y, u[s].z, u[s].w};
+      uint32_t top = 0;
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+#pragma unroll
+      for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int ef = (int)(top >> 7);                // biased exponent of the largest
+      if (top != 0 && ef != 255) {
+        const int e = max(ef, 1);                    // factor 2^(e - 127)
+        back = __uint_as_float((uint32_t)e << 23);
+        // 2^(127 - e); at e = 254 it has no normal encoding
+        mul *= e < 254 ? __uint_as_float((uint32_t)(254 - e) << 23) : __uint_as_float(1u << 22);
+      }
     }
-    const int ef = (int)(top >> 7);                  // biased exponent of the largest
-    if (top != 0 && ef != 255) {
-      const int e = max(ef, 1);                      // factor 2^(e - 127)
-      back = __uint_as_float((uint32_t)e << 23);
-      // 2^(127 - e), in two steps where it has no normal encoding
-      mul *= e < 254 ? __uint_as_float((uint32_t)(254 - e) << 23)
-                     : __uint_as_float(1u << 22);
-    }
-  }
-#pragma unroll 4
-  for (int c = 0; c < D / 8; ++c) {
     uint32_t h[4] = {0u, 0u, 0u, 0u};
-    if (live && mul != 0.f) {
+    if (sign != 0.f) {
       float f[8];
-      Vec<T>::to_f32(*reinterpret_cast<const uint4*>(src + 8 * c), f);
+      Vec<T>::to_f32(u[s], f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) h[k] = pack_half(f[2 * k] * mul, f[2 * k + 1] * mul);
     }
     const uint32_t dst = qbase + (c >> 3) * Ly::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                  ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    if (c == 0) factor[r] = back;
   }
-  return back;
 }
 
 // bytes of w that hold a NaN code (x.1111.111), as 0x80 in those bytes
@@ -405,17 +422,24 @@ __device__ __forceinline__ bool convert_tile(const ConvLane<D>& ln, uint32_t raw
 }
 
 // MMA issue (the MMA warp, converged; its elected lane issues). The whole of
-// tensor memory is allocated, so its base is 0. `alt`: the chains take the key tiles in turn (the
-// same Q tile); otherwise each takes every tile with its own Q tile. P comes
-// in two halves of 64 tokens. A
-// chain's weights lie over its scores, so its next scores are issued when its
-// last P V has completed; the other chain's softmax runs meanwhile.
-template <int D>
-__device__ void issue(int ntiles, bool alt, uint32_t tiles, uint32_t bar,
-                      volatile int* abort_flag) {
+// tensor memory is allocated, so its base is 0.
+//
+// A chain works in halves of a key tile, 64 tokens: scores, weights over
+// them, P V. That makes four streams (chain c, half h) whose S -> softmax ->
+// P V -> next S cycles overlap; a stream's next scores may only be written
+// once its P V has completed, so they are issued one step later, behind the
+// next stream's P V. ALT: the chains take the key tiles in turn (the same Q
+// tile); otherwise each takes every tile with its own Q tile.
+//
+// ALT and the tile count from a warp reduction keep the loop's control and
+// every operand warp-uniform for the compiler.
+template <int D, bool ALT>
+__device__ __forceinline__ void issue(int ntiles_any, uint32_t tiles, uint32_t bar,
+                                      volatile int* abort_flag) {
   using Ly = ChunkLayout<D>;
-  constexpr uint32_t idS = idesc_f16(false, kRows, kKv, false, false);
+  constexpr uint32_t idS = idesc_f16(false, kRows, kHalf, false, false);
   constexpr uint32_t idO = idesc_f16(false, kRows, D, false, true);
+  const int ntiles = __reduce_max_sync(0xffffffffu, ntiles_any);
   // descriptors of the first operands; the others differ by whole 16-byte
   // units in the address field (no carry: it counts the 227 KB of a CTA)
   const uint64_t q_desc = smem_desc_sw128(tiles + Ly::Q_OFF, 16, 1024);
@@ -426,71 +450,68 @@ __device__ void issue(int ntiles, bool alt, uint32_t tiles, uint32_t bar,
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar + 8u * b, parity & 1, abort_flag,
                                                      kWaitCycles));
   };
-  auto issue_s = [&](int c, int j) {              // chain c, tile j
+  constexpr int DJ = ALT ? 2 : 1;
+  constexpr int PER = ALT ? 2 : 4;                  // steps of a key tile
+  // scores of stream (c, h), tile j; the tile's last scores free its K
+  auto issue_s = [&](int c, int h, int j) {
+    if (h == 0 && (ALT || c == 0) &&
+        !wait(kKFull + (j & 1), j >> 1))            // first scores of the tile
+      return false;
     tc_fence_after();
-    const uint64_t qd = q_desc + (c == 1 && !alt ? (Ly::Q2_OFF - Ly::Q_OFF) >> 4 : 0);
-    const uint64_t kd = k_desc + (uint32_t)(j & 1) * (Ly::TILE >> 4);
+    const uint64_t qd = q_desc + (c == 1 && !ALT ? (Ly::Q2_OFF - Ly::Q_OFF) >> 4 : 0);
+    const uint64_t kd =
+        k_desc + (uint32_t)(j & 1) * (Ly::TILE >> 4) + h * (kHalf * 128 >> 4);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
       constexpr int step = Ly::HALF >> 4;
-      mma_f16_ss_if(leader, c * kKv, qd + (ks >> 2) * step + (ks & 3) * 2,
+      mma_f16_ss_if(leader, c * kKv + h * kHalf, qd + (ks >> 2) * step + (ks & 3) * 2,
                     kd + (ks >> 2) * step + (ks & 3) * 2, idS, ks > 0 ? 1u : 0u);
     }
-    mma_commit_if(leader, bar + 8u * (kSFull + c));
-    if (alt || c == 1) mma_commit_if(leader, bar + 8u * (kKEmpty + (j & 1)));
+    mma_commit_if(leader, bar + 8u * (kSFull + 2 * c + h));
+    if (h == 1 && (ALT || c == 1)) mma_commit_if(leader, bar + 8u * (kKEmpty + (j & 1)));
+    return true;
   };
-  auto issue_pv = [&](int c, int j, int h, bool first) {
+  auto issue_pv = [&](int c, int h, int j) {
     tc_fence_after();
     const uint64_t vd = v_desc + (uint32_t)(j & 1) * (Ly::TILE >> 4) + h * (kHalf * 128 >> 4);
     const uint32_t p = c * kKv + h * kHalf;
+    const uint32_t more = h > 0 || j >= DJ ? 1u : 0u;
 #pragma unroll
     for (int ks = 0; ks < kHalf / 16; ++ks)
       mma_f16_ts_if(leader, kOCol + c * kKv, p + ks * 8, vd + ks * (2048 >> 4), idO,
-                    (!first || ks > 0) ? 1u : 0u);
+                    ks > 0 ? 1u : more);
     mma_commit_if(leader, bar + 8u * (kODone + 2 * c + h));
-    if (h == 1 && (alt || c == 1)) mma_commit_if(leader, bar + 8u * (kVEmpty + (j & 1)));
+    if (h == 1 && (ALT || c == 1)) mma_commit_if(leader, bar + 8u * (kVEmpty + (j & 1)));
   };
+  // the stream of step x (of the round's tile i in {0, 1} when ALT)
+  auto chain_of = [](int i, int x) { return ALT ? i : x & 1; };
+  auto half_of = [](int x) { return ALT ? x : x >> 1; };
   bool ok = wait(kQFull, 0);
-  if (alt) {
-    for (int j = 0; ok && j < 2 && j < ntiles; ++j) {
-      ok = wait(kKFull + j, 0);
-      if (ok) issue_s(j, j);
-    }
-    for (int j = 0; ok && j < ntiles; ++j) {
-      const int c = j & 1, t = j >> 1;
-      ok = wait(kVFull + c, t) && wait(kPFull + 2 * c, t);
-      if (!ok) break;
-      issue_pv(c, j, 0, t == 0);
-      ok = wait(kPFull + 2 * c + 1, t);
-      if (!ok) break;
-      issue_pv(c, j, 1, false);
-      if (j + 2 < ntiles) {
-        ok = wait(kKFull + c, t + 1) && wait(kODone + 2 * c + 1, t);
-        if (ok) issue_s(c, j + 2);
-      }
-    }
-  } else {
-    ok = ok && wait(kKFull, 0);
-    if (ok) {
-      issue_s(0, 0);
-      issue_s(1, 0);
-    }
-    for (int j = 0; ok && j < ntiles; ++j) {
-      const bool more = j + 1 < ntiles;
-      ok = wait(kVFull + (j & 1), j >> 1);
-      if (ok && more) ok = wait(kKFull + ((j + 1) & 1), (j + 1) >> 1);
+  // first scores of the four streams, in the order of the steps
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        if (ok) ok = wait(kPFull + 2 * c, j);
+  for (int i = 0; i < DJ; ++i)
+#pragma unroll
+    for (int x = 0; x < PER; ++x)
+      if (ok && i < ntiles) ok = issue_s(chain_of(i, x), half_of(x), i);
+  for (int j0 = 0; ok && j0 < ntiles; j0 += DJ) {
+#pragma unroll
+    for (int i = 0; i < DJ; ++i) {
+      const int j = j0 + i;
+      if (!ok || j >= ntiles) break;
+      ok = wait(kVFull + (j & 1), j >> 1);
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int c = chain_of(i, x), h = half_of(x);
+        const int t = ALT ? j >> 1 : j;
+        if (ok) ok = wait(kPFull + 2 * c + h, t);
         if (!ok) break;
-        issue_pv(c, j, 0, j == 0);
-        ok = wait(kPFull + 2 * c + 1, j);
-        if (!ok) break;
-        issue_pv(c, j, 1, false);
-        if (more) {
-          ok = wait(kODone + 2 * c + 1, j);
-          if (ok) issue_s(c, j + 1);
-        }
+        issue_pv(c, h, j);
+        // the next scores of the step before this one
+        const int jl = x > 0 ? j : j - 1;
+        const int cl = x > 0 ? chain_of(i, x - 1) : chain_of(DJ - 1 - i, PER - 1);
+        const int hl = x > 0 ? half_of(x - 1) : half_of(PER - 1);
+        if (jl >= 0 && jl + DJ < ntiles)
+          ok = wait(kODone + 2 * cl + hl, ALT ? jl >> 1 : jl) && issue_s(cl, hl, jl + DJ);
       }
     }
   }
@@ -552,14 +573,14 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       mbar_init(bar + 8u * (kKEmpty + i), 1);
       mbar_init(bar + 8u * (kVFull + i), kConvWarps);
       mbar_init(bar + 8u * (kVEmpty + i), 1);
-      mbar_init(bar + 8u * (kSFull + i), 1);
     }
     for (int i = 0; i < 4; ++i) {
+      mbar_init(bar + 8u * (kSFull + i), 1);
       mbar_init(bar + 8u * (kPFull + i), 4);
       mbar_init(bar + 8u * (kODone + i), 1);
     }
     mbar_init(bar + 8u * kDone, 1);
-    mbar_init(bar + 8u * kQFull, kConvWarps);
+    mbar_init(bar + 8u * kQFull, 8);
     mbar_init(bar + 8u * kConvDone, kConvWarps);
     *abort_flag = 0;
     misc[6] = 0;                                    // NaN codes cleared in this CTA
@@ -595,25 +616,13 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     if (warp == kProducerWarp) {
       produce<D>(a, &tmK, &tmV, pc, kvh, tiles, bar, masks, abort_flag, raw_log2, lane);
     } else if (warp == kMmaWarp) {
-      if (tmem == 0) issue<D>(ntiles, alt, tiles, bar, abort_flag);
-      else *abort_flag = 1;
+      if (tmem != 0) *abort_flag = 1;
+      else if (alt) issue<D, true>(ntiles, tiles, bar, abort_flag);
+      else issue<D, false>(ntiles, tiles, bar, abort_flag);
       __syncwarp();
     } else if (warp >= kConvWarp) {
       const int cw = warp - kConvWarp;
       const ConvLane<D> ln(cw, lane);
-      for (int c = 0; c < (alt ? 1 : 2); ++c) {
-        const int r = cw * 32 + lane, rr = r0 + c * kRows + r;
-        const int i = rr / G;
-        const bool live = i < n;
-        const T* src =
-            reinterpret_cast<const T*>(a.q) +
-            ((int64_t)(q0 + (live ? i : 0)) * a.num_q_heads + (int64_t)kvh * G + rr % G) * D;
-        row_factor[c * kRows + r] = convert_q_row<T, D>(
-            src, live, a.scale, tiles + (c == 0 ? Ly::Q_OFF : Ly::Q2_OFF), r);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar + 8u * kQFull);
       for (int it = 0; it < 2 * ntiles; ++it) {
         int j;
         const bool isv = item_of(it, ntiles, &j);
@@ -656,6 +665,17 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t sadr = tmem + lanes + c * kKv;
     const uint32_t oadr = tmem + lanes + kOCol + c * kKv;
+    // the Q tiles: each chain its own, or both the one
+    if (alt)
+      convert_q_rows<T, D, G, 16>(a, q0, n, kvh, r0, (warp - kSoftmaxWarp) * 16,
+                                  tiles + Ly::Q_OFF, row_factor, lane);
+    else
+      convert_q_rows<T, D, G, 32>(a, q0, n, kvh, r0 + c * kRows, (warp & 3) * 32,
+                                  tiles + (c == 0 ? Ly::Q_OFF : Ly::Q2_OFF),
+                                  row_factor + c * kRows, lane);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + 8u * kQFull);
     bool ok = mbar_wait_bounded(bar + 8u * kQFull, 0, abort_flag, kWaitCycles);
     // logit factor in the log2 domain (Q carries the scale's sign and zero)
     const float f0 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e *
@@ -683,11 +703,6 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       float ks_next, vs_next;
       load_scales(ent_next, ks_next, vs_next);
       const int ent_2 = pc.entry(j + 2 * dj, lane);
-      if (ok)
-        ok = mbar_wait_bounded(bar + 8u * (kSFull + c), t & 1, abort_flag, kWaitCycles);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
       const bool whole = pm == full_mask && te - ts == kKv;
       const int hi = min(pos, te - 1) - ts;          // last column in sight
       const int first = lo - ts;                     // first column in sight
@@ -701,10 +716,14 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         }
         rcp_ref = vref > 0.f ? 1.f / vref : 0.f;
       }
-      // the tile in two steps of 64 tokens: the first half's P V runs while
-      // the second half's weights are made
+      // the tile in two steps of 64 tokens
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
+        if (ok)
+          ok = mbar_wait_bounded(bar + 8u * (kSFull + 2 * c + h), t & 1, abort_flag, kWaitCycles);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
         if (!idle) {
           uint32_t v[kHalf];
           tmem_ld64(sadr + h * kHalf, v);
@@ -819,6 +838,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         __syncwarp();
         if (lane == 0) mbar_arrive(bar + 8u * (kPFull + 2 * c + h));
       }
+      if (!ok) break;
       ent = ent_next;
       ent_next = ent_2;
       ksl = ks_next;
