@@ -108,6 +108,7 @@ struct ChunkLayout {
   static constexpr int SMEM = 3 * 1024 + TILES;
   static_assert(2 * RAW <= TILE, "two raw stages where Q tile 2 is");
   static_assert(kRows * D * 4 <= 2 * TILE, "the second chain's output where K is");
+  static_assert(2 * kRows * D * 2 <= 2 * TILE, "the output rows where V is");
   static_assert(SMALL <= 3 * 1024 - 16, "small region");
   static_assert(SMEM <= 232448, "over the shared memory of one CTA");
 };
@@ -276,9 +277,10 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtens
 // Q rows of a tile to fp16, each divided by the power of two of its largest
 // magnitude (bf16 only: fp16 queries are exact as they are); the sign of a
 // negative scale goes into Q, a zero scale makes it zero. `factor` gets what
-// was taken out of each row. A warp takes rows row0, row0 + 1, ... (a
-// multiple of 8 of them), 16 bytes per lane, so D / 8 lanes share a row; all
-// loads are issued before the first is used.
+// was taken out of each row. A warp takes ROWS rows from row0, D / 8 lanes to
+// a row: each lane copies its 16-byte pieces to their places asynchronously
+// (rows without a token are filled with zeros), then works on its own pieces
+// in place, several steps at a time: one step is a chain of some 400 clocks.
 template <typename T, int D, int G, int ROWS>
 __device__ __forceinline__ void convert_q_rows(const ChunkArgs& a, int q0, int n, int kvh,
                                                int tile_row0, int row0, uint32_t qbase,
@@ -288,48 +290,75 @@ __device__ __forceinline__ void convert_q_rows(const ChunkArgs& a, int q0, int n
   constexpr int RPS = 32 / LPR;                     // rows of a step
   constexpr int STEPS = ROWS / RPS;
   const int sub = lane / LPR, c = lane % LPR;
-  uint4 u[STEPS];
-#pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-    const int rr = tile_row0 + row0 + s * RPS + sub;
-    u[s] = make_uint4(0u, 0u, 0u, 0u);
-    if (rr / G < n)
-      u[s] = *reinterpret_cast<const uint4*>(
-          reinterpret_cast<const T*>(a.q) +
-          ((int64_t)(q0 + rr / G) * a.num_q_heads + (int64_t)kvh * G + rr % G) * D + 8 * c);
-  }
-  const float sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
-#pragma unroll
+  const uint32_t dst0 = qbase + (c >> 3) * Ly::HALF;
+#pragma unroll 4
   for (int s = 0; s < STEPS; ++s) {
     const int r = row0 + s * RPS + sub;
-    float mul = sign, back = 1.f;
+    const int rr = tile_row0 + r;
+    const bool live = rr / G < n;
+    const T* src =
+        reinterpret_cast<const T*>(a.q) +
+        ((int64_t)(q0 + (live ? rr / G : 0)) * a.num_q_heads + (int64_t)kvh * G + rr % G) * D +
+        8 * c;
+    const uint32_t dst = dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 ::"r"(dst), "l"(src), "r"(live ? 16u : 0u) : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  const float sign = a.scale < 0.f ? -1.f : a.scale == 0.f ? 0.f : 1.f;
+  constexpr int AT_ONCE = STEPS < 8 ? STEPS : 8;
+#pragma unroll 1
+  for (int s0 = 0; s0 < STEPS; s0 += AT_ONCE) {
+    const int r0 = row0 + s0 * RPS + sub;             // rows of the steps: RPS apart
+    uint4 u[AT_ONCE];
+    uint32_t top[AT_ONCE];
+#pragma unroll
+    for (int s = 0; s < AT_ONCE; ++s) {
+      const int r = r0 + s * RPS;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(u[s].x), "=r"(u[s].y), "=r"(u[s].z), "=r"(u[s].w)
+                   : "r"(dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)));
+    }
     if (std::is_same<T, __nv_bfloat16>::value) {
-      const uint32_t w[4] = {u[s].x, u[s].y, u[s].z, u[s].w};
-      uint32_t top = 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        top = max(top, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+      for (int s = 0; s < AT_ONCE; ++s) {
+        const uint32_t w[4] = {u[s].x, u[s].y, u[s].z, u[s].w};
+        top[s] = 0;
 #pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int ef = (int)(top >> 7);                // biased exponent of the largest
-      if (top != 0 && ef != 255) {
-        const int e = max(ef, 1);                    // factor 2^(e - 127)
-        back = __uint_as_float((uint32_t)e << 23);
-        // 2^(127 - e); at e = 254 it has no normal encoding
-        mul *= e < 254 ? __uint_as_float((uint32_t)(254 - e) << 23) : __uint_as_float(1u << 22);
+        for (int k = 0; k < 4; ++k)
+          top[s] = max(top[s], max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
       }
-    }
-    uint32_t h[4] = {0u, 0u, 0u, 0u};
-    if (sign != 0.f) {
-      float f[8];
-      Vec<T>::to_f32(u[s], f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) h[k] = pack_half(f[2 * k] * mul, f[2 * k + 1] * mul);
+      for (int o = 1; o < LPR; o <<= 1)
+#pragma unroll
+        for (int s = 0; s < AT_ONCE; ++s)
+          top[s] = max(top[s], __shfl_xor_sync(0xffffffffu, top[s], o));
     }
-    const uint32_t dst = qbase + (c >> 3) * Ly::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
-                 ::"r"(dst), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-    if (c == 0) factor[r] = back;
+#pragma unroll
+    for (int s = 0; s < AT_ONCE; ++s) {
+      const int r = r0 + s * RPS;
+      float mul = sign, back = 1.f;
+      if (std::is_same<T, __nv_bfloat16>::value) {
+        const int ef = (int)(top[s] >> 7);           // biased exponent of the largest
+        if (top[s] != 0 && ef != 255) {
+          const int e = max(ef, 1);                  // factor 2^(e - 127)
+          back = __uint_as_float((uint32_t)e << 23);
+          // 2^(127 - e); at e = 254 it has no normal encoding
+          mul *= __uint_as_float(e < 254 ? (uint32_t)(254 - e) << 23 : 1u << 22);
+        }
+      }
+      uint32_t h[4] = {0u, 0u, 0u, 0u};
+      if (sign != 0.f) {
+        float f[8];
+        Vec<T>::to_f32(u[s], f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = pack_half(f[2 * k] * mul, f[2 * k + 1] * mul);
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
+                   ::"r"(dst0 + r * 128 + (((c & 7) ^ (r & 7)) << 4)), "r"(h[0]), "r"(h[1]),
+                     "r"(h[2]), "r"(h[3]) : "memory");
+      if (c == 0) factor[r] = back;
+    }
   }
 }
 
@@ -892,8 +921,11 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       const float mul1 = unit * w1 * inv, mul2 = w2 * inv;
       const bool second = alt && ntiles > 1 && w2 != 0.f;
       const bool nans = misc[6] != 0;
-      T* out = reinterpret_cast<T*>(a.out);
       const int64_t slot = (tok * a.num_q_heads + head) * a.num_splits + split;
+      // where the V tiles were: 32 rows of this warp
+      constexpr int OUTS = D / 8;                    // 16-byte pieces of an output row
+      uint4* strip = reinterpret_cast<uint4*>(smem_raw + (tiles - sbase) + Ly::V_OFF) +
+                     (warp - kSoftmaxWarp) * 32 * OUTS;
 #pragma unroll 1
       for (int ch = 0; ch < D / 32; ++ch) {
         const int c0 = ch * 32;
@@ -936,7 +968,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             if ((bad >> e) & 1u) o[e] = 0x7fffffffu;
         }
         if (direct) {
-          uint4* op = reinterpret_cast<uint4*>(out + (tok * a.num_q_heads + head) * D + c0);
+          // own row to this warp's strip, 16-byte pieces spread over the banks
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             uint4 w;
@@ -944,7 +976,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             w.y = pack_out<T>(__uint_as_float(o[8 * q + 2]), __uint_as_float(o[8 * q + 3]));
             w.z = pack_out<T>(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5]));
             w.w = pack_out<T>(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7]));
-            op[q] = w;
+            strip[lane * OUTS + ((ch * 4 + q) ^ (lane & 7))] = w;
           }
         } else if (partial) {
           uint4* acc = reinterpret_cast<uint4*>(a.ws_acc + slot * D + c0);
@@ -956,6 +988,20 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       if (partial) {
         a.ws_ml[2 * slot] = m_use;
         a.ws_ml[2 * slot + 1] = l;
+      }
+      if (sp.count == 1) {
+        // whole rows to memory: a row per D / 8 lanes
+        T* out = reinterpret_cast<T*>(a.out);
+        __syncwarp();
+#pragma unroll 4
+        for (int x = lane; x < 32 * OUTS; x += 32) {
+          const int wr = x / OUTS, q = x % OUTS;
+          const int row = rr - lane + wr;            // row of the sequence
+          if (row / G < n)
+            reinterpret_cast<uint4*>(
+                out + ((int64_t)(q0 + row / G) * a.num_q_heads + kvh * G + row % G) * D)[q] =
+                strip[wr * OUTS + (q ^ (wr & 7))];
+        }
       }
     }
   }
