@@ -452,9 +452,14 @@ def pa_decode_attention_fp8_window(q: torch.Tensor, key_cache: torch.Tensor,
                         window, out, max_seq_len, partition_size, workspace, stream)
 
 
-def _here(t: torch.Tensor, name: str, dtype=None, shape=None, dense=True):
-    """_dev plus the current device and the shape; dense=False leaves the
-    strides to the caller."""
+def _current() -> tuple:
+    """(current device index, its current stream as an integer)."""
+    dev = torch._C._cuda_getDevice()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _refuse(t: torch.Tensor, name: str, dtype, shape, dense: bool):
+    """Say what is wrong with t; None if nothing is."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.device.index != torch.cuda.current_device():
@@ -463,16 +468,29 @@ def _here(t: torch.Tensor, name: str, dtype=None, shape=None, dense=True):
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _buffer(t, name, dtype, shape, device):
+def _want(dev: int, t: torch.Tensor, name: str, dtype, *shape) -> int:
+    """Address of t, which must be a dense tensor of this dtype and shape on
+    the current device. A step makes a dozen of these checks, and small steps
+    are bound by them: the passing path asks for as little as it can."""
+    if (t.get_device() != dev or t.dtype != dtype or t.shape != shape
+            or not t.is_contiguous()):
+        _refuse(t, name, dtype, shape, True)
+    return t.data_ptr()
+
+
+def _buffer(t, name, dtype, device, dev, *shape):
     """The caller's output buffer, checked, or a new one."""
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _here(t, name, dtype, shape)
+    _want(dev, t, name, dtype, *shape)
     return t
+
+
+_I32, _I64, _U8, _F32, _F64 = torch.int32, torch.int64, torch.uint8, torch.float32, torch.float64
 
 
 def pa_extend_block_tables(context_lens: torch.Tensor, new_tokens: torch.Tensor,
@@ -493,30 +511,39 @@ def pa_extend_block_tables(context_lens: torch.Tensor, new_tokens: torch.Tensor,
     may be context_lens. Returns (query_start_loc, block_start_loc, seq_lens,
     positions, slot_mapping). A step that lacks blocks changes nothing and
     latches PA_ERR_NO_BLOCKS."""
-    S, dev = context_lens.numel(), context_lens.device
-    i32, i64 = torch.int32, torch.int64
-    _here(context_lens, "context_lens", i32, (S,))
-    _here(new_tokens, "new_tokens", i32, (S,))
-    _here(block_tables, "block_tables", i32)
-    _here(free_ring, "free_ring", i32)
-    _here(ring_state, "ring_state", i64, (2,))
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    T = int(num_tokens)
+    if not context_lens.is_cuda:
+        raise ValueError("context_lens must be a CUDA tensor")
+    dev, st = _current()
+    S, T, where = context_lens.numel(), int(num_tokens), context_lens.device
     if T < 0:
         raise ValueError("num_tokens must not be negative")
-    ring_state_out = (ring_state if ring_state_out is None else
-                      _buffer(ring_state_out, "ring_state_out", i64, (2,), dev))
-    query_start_loc = _buffer(query_start_loc, "query_start_loc", i32, (S + 1,), dev)
-    block_start_loc = _buffer(block_start_loc, "block_start_loc", i32, (S + 1,), dev)
-    seq_lens = _buffer(seq_lens, "seq_lens", i32, (S,), dev)
-    positions = _buffer(positions, "positions", i64, (T,), dev)
-    slot_mapping = _buffer(slot_mapping, "slot_mapping", i64, (T,), dev)
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, max_blocks]")
+    cols, R = block_tables.shape[1], free_ring.numel()
+    if ring_state_out is None:
+        ring_state_out = ring_state
+    if query_start_loc is None:
+        query_start_loc = torch.empty(S + 1, dtype=_I32, device=where)
+    if block_start_loc is None:
+        block_start_loc = torch.empty(S + 1, dtype=_I32, device=where)
+    if seq_lens is None:
+        seq_lens = torch.empty(S, dtype=_I32, device=where)
+    if positions is None:
+        positions = torch.empty(T, dtype=_I64, device=where)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(T, dtype=_I64, device=where)
     check("pa_extend_block_tables", lib().pa_extend_block_tables(
-        ptr(context_lens), ptr(new_tokens), S, ptr(block_tables), block_tables.shape[1],
-        int(block_size), int(num_blocks), ptr(free_ring), free_ring.numel(), ptr(ring_state),
-        ptr(ring_state_out), T, ptr(query_start_loc), ptr(block_start_loc), ptr(seq_lens),
-        ptr(positions), ptr(slot_mapping), stream_handle(stream)))
+        _want(dev, context_lens, "context_lens", _I32, S),
+        _want(dev, new_tokens, "new_tokens", _I32, S), S,
+        _want(dev, block_tables, "block_tables", _I32, S, cols), cols, int(block_size),
+        int(num_blocks), _want(dev, free_ring, "free_ring", _I32, R), R,
+        _want(dev, ring_state, "ring_state", _I64, 2),
+        _want(dev, ring_state_out, "ring_state_out", _I64, 2), T,
+        _want(dev, query_start_loc, "query_start_loc", _I32, S + 1),
+        _want(dev, block_start_loc, "block_start_loc", _I32, S + 1),
+        _want(dev, seq_lens, "seq_lens", _I32, S), _want(dev, positions, "positions", _I64, T),
+        _want(dev, slot_mapping, "slot_mapping", _I64, T),
+        st if stream is None else stream.cuda_stream))
     return query_start_loc, block_start_loc, seq_lens, positions, slot_mapping
 
 
@@ -531,70 +558,81 @@ def pa_release_block_tables(finished: torch.Tensor, seq_lens: torch.Tensor,
     of the free ring and set their lengths to 0. ring_state_out and
     seq_lens_out default to in place. Returns release_start_loc int32 [S + 1]:
     where each request's blocks begin among those returned."""
-    S, dev = seq_lens.numel(), seq_lens.device
-    i32, i64 = torch.int32, torch.int64
+    if not seq_lens.is_cuda:
+        raise ValueError("seq_lens must be a CUDA tensor")
+    dev, st = _current()
+    S = seq_lens.numel()
     if finished.dtype == torch.bool:
-        finished = finished.view(torch.uint8)
-    _here(finished, "finished", torch.uint8, (S,))
-    _here(seq_lens, "seq_lens", i32, (S,))
-    _here(block_tables, "block_tables", i32)
-    _here(free_ring, "free_ring", i32)
-    _here(ring_state, "ring_state", i64, (2,))
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        finished = finished.view(_U8)
+    if block_tables.dim() != 2:
         raise ValueError("block_tables must be [num_seqs, max_blocks]")
-    ring_state_out = (ring_state if ring_state_out is None else
-                      _buffer(ring_state_out, "ring_state_out", i64, (2,), dev))
-    seq_lens_out = (seq_lens if seq_lens_out is None else
-                    _buffer(seq_lens_out, "seq_lens_out", i32, (S,), dev))
-    release_start_loc = _buffer(release_start_loc, "release_start_loc", i32, (S + 1,), dev)
+    cols, R = block_tables.shape[1], free_ring.numel()
+    if ring_state_out is None:
+        ring_state_out = ring_state
+    if seq_lens_out is None:
+        seq_lens_out = seq_lens
+    if release_start_loc is None:
+        release_start_loc = torch.empty(S + 1, dtype=_I32, device=seq_lens.device)
     check("pa_release_block_tables", lib().pa_release_block_tables(
-        ptr(finished), ptr(seq_lens), S, ptr(block_tables), block_tables.shape[1],
-        int(block_size), int(num_blocks), ptr(free_ring), free_ring.numel(), ptr(ring_state),
-        ptr(ring_state_out), ptr(release_start_loc), ptr(seq_lens_out), stream_handle(stream)))
+        _want(dev, finished, "finished", _U8, S), _want(dev, seq_lens, "seq_lens", _I32, S), S,
+        _want(dev, block_tables, "block_tables", _I32, S, cols), cols, int(block_size),
+        int(num_blocks), _want(dev, free_ring, "free_ring", _I32, R), R,
+        _want(dev, ring_state, "ring_state", _I64, 2),
+        _want(dev, ring_state_out, "ring_state_out", _I64, 2),
+        _want(dev, release_start_loc, "release_start_loc", _I32, S + 1),
+        _want(dev, seq_lens_out, "seq_lens_out", _I32, S),
+        st if stream is None else stream.cuda_stream))
     return release_start_loc
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype):
-    """[T, H, D] whose tokens may be apart (a slice of a fused projection)."""
-    _here(t, name, dtype, shape, dense=False)
+def _rows(dev: int, t: torch.Tensor, name: str, dtype, shape) -> tuple:
+    """(address, elements between tokens) of t [T, H, D] with dense heads;
+    tokens may be apart (a slice of a fused projection)."""
     T, H, D = shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape:
+        _refuse(t, name, dtype, shape, False)
+    row, head, one = t.stride()
+    if (one != 1 and D > 1) or (head != D and H > 1):
         raise ValueError(f"{name} must have dense rows [heads, head_size]")
-    return t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), row if T > 1 else H * D
 
 
 def _rotary_call(name, q, k, v, positions, inv_freq, slot_mapping, key_cache, value_cache,
                  pool_dtype, scales, axis_of_pair, interleaved, q_out, stream):
     if q.dim() != 3 or k.dim() != 3 or key_cache.dim() != 4:
         raise ValueError("q and k must be [T, heads, head_size], pools [NB, Hkv, B, D]")
-    T, Hq, D = q.shape
-    NB, Hkv, B, Dk = key_cache.shape
-    if Dk != D or value_cache.shape != key_cache.shape:
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev, st = _current()
+    T, Hq, D = shape = q.shape
+    NB, Hkv, B, Dk = pool = key_cache.shape
+    dtype = q.dtype
+    code = DTYPE_CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"q must be float32, float16 or bfloat16, got {dtype}")
+    if Dk != D:
         raise ValueError("pool shape does not match q")
-    if q.dtype not in DTYPE_CODE:
-        raise ValueError(f"q must be float32, float16 or bfloat16, got {q.dtype}")
-    qs = _rows(q, "q", (T, Hq, D), q.dtype)
-    ks = _rows(k, "k", (T, Hkv, D), q.dtype)
-    vs = _rows(v, "v", (T, Hkv, D), q.dtype)
-    _here(key_cache, "key_cache", pool_dtype)
-    _here(value_cache, "value_cache", pool_dtype)
-    _here(slot_mapping, "slot_mapping", torch.int64, (T,))
-    _here(positions, "positions", torch.int64)
-    if positions.shape[-1:] != (T,) or positions.dim() not in (1, 2):
+    if positions.dim() == 1:
+        axes, pos = 1, _want(dev, positions, "positions", _I64, T)
+    elif positions.dim() == 2:
+        axes = positions.shape[0]
+        pos = _want(dev, positions, "positions", _I64, axes, T)
+    else:
         raise ValueError("positions must be [T] or [axes, T]")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
     half = inv_freq.numel()
-    _here(inv_freq, "inv_freq", torch.float64, (half,))
-    if axis_of_pair is not None:
-        _here(axis_of_pair, "axis_of_pair", torch.int32, (half,))
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    qo = _rows(q_out, "q_out", (T, Hq, D), q.dtype)
+        q_out = torch.empty(shape, dtype=dtype, device=q.device)
+    kv = (T, Hkv, D)
     check(name, getattr(lib(), name)(
-        ptr(q), qs, ptr(k), ks, ptr(v), vs, T, Hq, Hkv, D, DTYPE_CODE[q.dtype], ptr(positions), T,
-        axes, ptr(inv_freq), ptr(axis_of_pair), 2 * half, int(bool(interleaved)),
-        ptr(slot_mapping), ptr(q_out), qo, ptr(key_cache), ptr(value_cache), NB, B, *scales,
-        stream_handle(stream)))
+        *_rows(dev, q, "q", dtype, shape), *_rows(dev, k, "k", dtype, kv),
+        *_rows(dev, v, "v", dtype, kv), T, Hq, Hkv, D, code, pos, T, axes,
+        _want(dev, inv_freq, "inv_freq", _F64, half),
+        None if axis_of_pair is None else _want(dev, axis_of_pair, "axis_of_pair", _I32, half),
+        2 * half, 1 if interleaved else 0, _want(dev, slot_mapping, "slot_mapping", _I64, T),
+        *_rows(dev, q_out, "q_out", dtype, shape),
+        _want(dev, key_cache, "key_cache", pool_dtype, *pool),
+        _want(dev, value_cache, "value_cache", pool_dtype, *pool), NB, B, *scales,
+        st if stream is None else stream.cuda_stream))
     return q_out
 
 
@@ -645,12 +683,13 @@ def pa_rotary_reshape_and_cache_fp8_scaled(q: torch.Tensor, k: torch.Tensor, v: 
     """pa_rotary_reshape_and_cache into E4M3 pools whose blocks carry their
     own scales (float32 [NB, Hkv]), updated where this write stores a block's
     first row."""
-    want = tuple(key_cache.shape[:2])
-    _here(k_scales, "k_scales", torch.float32, want)
-    _here(v_scales, "v_scales", torch.float32, want)
+    NB, Hkv = key_cache.shape[:2]
+    dev = key_cache.get_device()
+    scales = (_want(dev, k_scales, "k_scales", _F32, NB, Hkv),
+              _want(dev, v_scales, "v_scales", _F32, NB, Hkv))
     return _rotary_call("pa_rotary_reshape_and_cache_fp8_scaled", q, k, v, positions, inv_freq,
                         slot_mapping, key_cache, value_cache, torch.uint8,
-                        (ptr(k_scales), ptr(v_scales)), axis_of_pair, interleaved, q_out, stream)
+                        scales, axis_of_pair, interleaved, q_out, stream)
 
 
 def pa_multi_query_fp8_workspace_bytes(num_tokens: int, num_seqs: int, num_q_heads: int,
@@ -671,38 +710,39 @@ def _chunk_call(name, q, query_start_loc, key_cache, value_cache, scale_tensors,
                 window, partition_size, workspace, stream):
     if q.dim() != 3 or key_cache.dim() != 4 or block_tables.dim() != 2:
         raise ValueError("q must be [T, Hq, D], pools [NB, Hkv, B, D], block_tables [S, blocks]")
-    T, Hq, D = q.shape
-    NB, Hkv, B, Dk = key_cache.shape
-    S = seq_lens.numel()
-    if q.dtype not in DTYPE_CODE:
-        raise ValueError(f"q must be float16 or bfloat16, got {q.dtype}")
-    if Hkv != num_kv_heads or Dk != D or value_cache.shape != key_cache.shape:
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    dev, st = _current()
+    T, Hq, D = shape = q.shape
+    NB, Hkv, B, Dk = pool = key_cache.shape
+    S, cols = seq_lens.numel(), block_tables.shape[1]
+    dtype = q.dtype
+    code = DTYPE_CODE.get(dtype)
+    if code is None:
+        raise ValueError(f"q must be float16 or bfloat16, got {dtype}")
+    if Hkv != num_kv_heads or Dk != D:
         raise ValueError("pool shape does not match q / num_kv_heads")
-    _here(q, "q")
-    _here(key_cache, "key_cache", torch.uint8)
-    _here(value_cache, "value_cache", torch.uint8)
-    _here(query_start_loc, "query_start_loc", torch.int32, (S + 1,))
-    _here(seq_lens, "seq_lens", torch.int32, (S,))
-    _here(block_tables, "block_tables", torch.int32)
-    if block_tables.shape[0] != S:
-        raise ValueError("block_tables must have one row per sequence")
-    for t in scale_tensors:
-        _here(t, "scales", torch.float32, (NB, Hkv))
-    out = _buffer(out, "out", q.dtype, (T, Hq, D), q.device)
+    out = _buffer(out, "out", dtype, q.device, dev, *shape)
     if workspace is None:
         need = pa_multi_query_fp8_workspace_bytes(T, S, Hq, Hkv, D, B, max_query_len, max_seq_len,
                                                   window, partition_size)
         if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    else:
-        _here(workspace, "workspace")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+            workspace = torch.empty(need, dtype=_U8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        _refuse(workspace, "workspace", None, None, True)
     check(name, getattr(lib(), name)(
-        ptr(q), ptr(query_start_loc), S, T, ptr(key_cache), ptr(value_cache),
-        *[ptr(t) for t in scale_tensors], ptr(block_tables), block_tables.shape[1], ptr(seq_lens),
-        Hq, Hkv, D, B, NB, DTYPE_CODE[q.dtype], float(scale), *scale_values, int(window),
-        int(max_query_len), int(max_seq_len), int(partition_size), ptr(out), ptr(workspace),
-        ws_bytes, stream_handle(stream)))
+        _want(dev, q, "q", dtype, *shape),
+        _want(dev, query_start_loc, "query_start_loc", _I32, S + 1), S, T,
+        _want(dev, key_cache, "key_cache", _U8, *pool),
+        _want(dev, value_cache, "value_cache", _U8, *pool),
+        *[_want(dev, t, "scales", _F32, NB, Hkv) for t in scale_tensors],
+        _want(dev, block_tables, "block_tables", _I32, S, cols), cols,
+        _want(dev, seq_lens, "seq_lens", _I32, S), Hq, Hkv, D, B, NB, code, float(scale),
+        *scale_values, int(window), int(max_query_len), int(max_seq_len), int(partition_size),
+        out.data_ptr(),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.nbytes,
+        st if stream is None else stream.cuda_stream))
     return out
 
 
