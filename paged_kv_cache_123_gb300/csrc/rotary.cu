@@ -10,9 +10,8 @@
 // once, from fp32 to the stored type.
 //
 // Angles: a far position times a frequency needs more than fp32, and FP64
-// products and range reductions per angle would load the few FP64 units. The
-// frequency becomes a 64-bit fixed-point fraction of a turn once per thread
-// (two FP64 products, exact to 2^-64 of a turn); position x fraction in
+// products and range reductions per angle would load the few FP64 units. A
+// frequency becomes a 64-bit fixed-point fraction of a turn; position x fraction in
 // wrapping 64-bit integers then IS the reduction to one turn, and the top 32
 // bits go to sincospif as half turns in [-1, 1).
 //
@@ -22,6 +21,8 @@
 // and then runs over (token, head) rows; a thread keeps its place in the
 // row, so its cosines change only with the token.
 #include <cuda_fp8.h>
+
+#include <algorithm>
 
 #include "block_scale.cuh"
 #include "common.cuh"
@@ -33,15 +34,28 @@ namespace {
 constexpr int kRotThreads = 256;
 constexpr int kRotMaxHalf = 128;     // head_size <= 256
 
-// inv_freq as a fraction of a turn, 64-bit fixed point: x / (2 pi) with the
-// reciprocal split in two doubles, its whole turns dropped.
+// x as a fraction of a turn, x / (2 pi) mod 1, in 64-bit fixed point: the
+// 53-bit mantissa times the first 128 bits of 1 / (2 pi), shifted by the
+// exponent. Off by less than 2^-64 of a turn for |x| < 2^62; 0 for zeros,
+// subnormals, infinities and NaN. In integers, because the SM has few FP64
+// units: a warp's FP64 instruction occupies them for 16 clocks.
 __device__ __forceinline__ uint64_t turn_fraction(double x) {
-  const double hi = 0.15915494309189535, lo = -9.839338337591243e-18;   // 1 / (2 pi)
-  const double p = x * hi;
-  const double e = fma(x, hi, -p) + x * lo;
-  const double f = p - floor(p);                    // exact
-  const uint64_t whole = __double2ull_rz(f * 18446744073709551616.0);
-  return whole + (uint64_t)__double2ll_rn(e * 18446744073709551616.0);
+  const uint64_t c_hi = 0x28be60db9391054aull, c_lo = 0x7f09d5f47d4d3770ull;
+  const uint64_t bits = (uint64_t)__double_as_longlong(x);
+  const int e = (int)(bits >> 52) & 0x7ff;
+  const uint64_t m = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  // 192-bit product m * (c_hi 2^64 + c_lo), limbs p0 (low) to p2
+  const uint64_t p0 = m * c_lo, mid = __umul64hi(m, c_lo), q = m * c_hi;
+  const uint64_t p1 = mid + q;
+  const uint64_t p2 = __umul64hi(m, c_hi) + (p1 < q ? 1u : 0u);
+  // the 64 bits from bit s on
+  const int s = 1139 - e;
+  if (e == 0 || e == 0x7ff || s < 0 || s >= 192) return 0;
+  const uint64_t a = s < 64 ? p0 : s < 128 ? p1 : p2;
+  const uint64_t b = s < 64 ? p1 : s < 128 ? p2 : 0;
+  const int k = s & 63;
+  const uint64_t r = k == 0 ? a : (a >> k) | (b << (64 - k));
+  return (bits >> 63) != 0 ? 0 - r : r;
 }
 
 __device__ __forceinline__ float2 cos_sin(int64_t pos, uint64_t turn) {
@@ -68,9 +82,12 @@ __device__ __forceinline__ uint4 pack16(const float* f) {
 }
 
 // N fp32 values divided by the scale (IEEE fp32) to N E4M3 codes, nearest
-// even, saturating
-template <int N>
+// even, saturating. POW2: the scale is a power of two, whose reciprocal is
+// exact, so a product gives the quotient.
+template <int N, bool POW2>
 __device__ __forceinline__ void store_fp8(uint8_t* dst, const float* f, float scale) {
+  const float rcp = POW2 ? 1.f / scale : 0.f;
+  auto over = [&](float x) { return POW2 ? x * rcp : __fdiv_rn(x, scale); };
   uint32_t w[N / 4];
 #pragma unroll
   for (int j = 0; j < N / 4; ++j) {
@@ -78,8 +95,8 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, const float* f, float sc
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const __nv_fp8x2_storage_t p = __nv_cvt_float2_to_fp8x2(
-          make_float2(__fdiv_rn(f[4 * j + 2 * h], scale), __fdiv_rn(f[4 * j + 2 * h + 1], scale)),
-          __NV_SATFINITE, __NV_E4M3);
+          make_float2(over(f[4 * j + 2 * h]), over(f[4 * j + 2 * h + 1])), __NV_SATFINITE,
+          __NV_E4M3);
       a |= (uint32_t)p << (16 * h);
     }
     w[j] = a;
@@ -92,7 +109,8 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, const float* f, float sc
 // c < rot / (2N) holds N pairs, the vectors at c*N and rot/2 + c*N (halves)
 // or the neighbours at 2c*N and 2c*N + N (interleaved), later units the
 // neighbours at 2c*N (dims that pass).
-template <typename T, bool FP8, bool INTER, int TOK>
+// POOL: 0 pools of T, 1 E4M3 with one scale, 2 E4M3 with per-block scales.
+template <typename T, int POOL, bool INTER, int TOK>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a) {
   constexpr int N = Vec<T>::N;
   __shared__ float2 cs[TOK][kRotMaxHalf];
@@ -166,13 +184,13 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
           const int64_t blk = slot / a.block_size;
           const int64_t dst =
               ((blk * a.num_kv_heads + kvh) * a.block_size + (slot - blk * a.block_size)) * D;
-          if (FP8) {
-            float sc = kind == 1 ? a.k_scale : a.v_scale;
-            if (a.k_scales != nullptr)
-              sc = (kind == 1 ? a.k_scales : a.v_scales)[blk * a.num_kv_heads + kvh];
+          if (POOL != 0) {
+            const float sc =
+                POOL == 2 ? (kind == 1 ? a.k_scales : a.v_scales)[blk * a.num_kv_heads + kvh]
+                          : (kind == 1 ? a.k_scale : a.v_scale);
             uint8_t* cache = (uint8_t*)(kind == 1 ? a.kc : a.vc) + dst;
-            store_fp8<N>(cache + e0, x, sc);
-            store_fp8<N>(cache + e1, x + N, sc);
+            store_fp8<N, POOL == 2>(cache + e0, x, sc);
+            store_fp8<N, POOL == 2>(cache + e1, x + N, sc);
           } else {
             T* cache = (T*)(kind == 1 ? a.kc : a.vc) + dst;
             *reinterpret_cast<uint4*>(cache + e0) = pack16<T>(x);
@@ -186,95 +204,154 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
 }
 
 // First pass of the write into pools with per-block scales, as
-// fix_block_scales_kernel of the plain write: one warp per (token, KV head)
-// whose slot is row 0 of its block takes the largest magnitude over the run
-// of tokens that this call puts into the block, of the ROTATED keys and of
-// the values, and fixes the block's scales. A lane owns pairs lane, lane +
-// 32, ..., so it needs their frequencies only once.
+// fix_block_scales_kernel of the plain write: for each token whose slot is
+// row 0 of its block, the largest magnitude over the run of tokens that this
+// call puts into the block, of the ROTATED keys and of the values, fixes the
+// block's scales. A CTA looks at kScaleTokens tokens and takes the runs that
+// begin there one after the other: the run's cosines and sines go to shared
+// memory, kRunTokens tokens at a time, and each warp takes KV heads, in the
+// units of rotary_kernel (the same arithmetic, so the maximum is of exactly
+// the values that the second pass quantises).
+constexpr int kScaleTokens = 16;
+constexpr int kRunTokens = 16;
+constexpr int kHeadsPerWarp = 8;
+
 template <typename T, bool INTER>
 __global__ void __launch_bounds__(kRotThreads) rotary_scales_kernel(const RotaryArgs a) {
-  constexpr int kMaxPairs = kRotMaxHalf / 32;
+  constexpr int N = Vec<T>::N;
+  constexpr int WARPS = kRotThreads / 32;
+  __shared__ float2 cs[kRunTokens][kRotMaxHalf];
+  __shared__ uint64_t turn[kRotMaxHalf];
+  __shared__ int axis[kRotMaxHalf];
+  __shared__ int64_t first_slot[kScaleTokens];
+  __shared__ int run_len;
   griddep_launch();
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int half = a.rot_size / 2, D = a.head_size;
-  const int64_t warps = (int64_t)gridDim.x * (kRotThreads / 32);
-  const int64_t limit = a.num_blocks * a.block_size;
-  uint64_t turn[kMaxPairs];
-  int axis[kMaxPairs];
-#pragma unroll
-  for (int j = 0; j < kMaxPairs; ++j) {
-    const int p = lane + 32 * j;
-    turn[j] = p < half ? turn_fraction(a.inv_freq[p]) : 0;
-    axis[j] = p < half && a.axis_of_pair != nullptr ? a.axis_of_pair[p] : 0;
-    if (axis[j] < 0 || axis[j] >= a.num_axes) axis[j] = 0;    // reported by the second pass
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int half = a.rot_size / 2, D = a.head_size, B = a.block_size;
+  const int units = D / (2 * N), rot_units = a.rot_size / (2 * N);
+  const int rows_at_once = 32 / units;
+  const int c = lane % units, lane_row = lane / units;
+  const bool rot = c < rot_units;
+  const int e0 = rot && !INTER ? c * N : 2 * c * N;
+  const int e1 = rot && !INTER ? half + c * N : e0 + N;
+  const int64_t limit = a.num_blocks * B;
+  const int64_t base = (int64_t)blockIdx.x * kScaleTokens;
+  for (int p = threadIdx.x; p < half; p += kRotThreads) {
+    turn[p] = turn_fraction(a.inv_freq[p]);
+    const int ax = a.axis_of_pair != nullptr ? a.axis_of_pair[p] : 0;
+    axis[p] = ax < 0 || ax >= a.num_axes ? 0 : ax;    // reported by the second pass
   }
-  for (int64_t w = (int64_t)blockIdx.x * (kRotThreads / 32) + (threadIdx.x >> 5);
-       w < a.num_tokens * a.num_kv_heads; w += warps) {
-    const int64_t t = w / a.num_kv_heads;
-    const int h = (int)(w - t * a.num_kv_heads);
-    const int64_t s0 = a.slots[t];
-    if (s0 < 0 || s0 >= limit || s0 % a.block_size != 0) continue;
-    int n = 1;
-    while (n < a.block_size && t + n < a.num_tokens && a.slots[t + n] == s0 + n) ++n;
-    float ka = 0.f, va = 0.f;
-    for (int r = 0; r < n; ++r) {
-      const T* k = (const T*)a.k + (t + r) * a.k_stride + (int64_t)h * D;
-      const T* v = (const T*)a.v + (t + r) * a.v_stride + (int64_t)h * D;
+  if (threadIdx.x < kScaleTokens) {
+    const int64_t s = base + threadIdx.x < a.num_tokens ? a.slots[base + threadIdx.x] : -1;
+    // only slots that begin a block; those past the pool are reported by the
+    // second pass
+    first_slot[threadIdx.x] = s >= 0 && s < limit && s % B == 0 ? s : -1;
+  }
+  __syncthreads();
+  for (int i = 0; i < kScaleTokens; ++i) {
+    const int64_t s0 = first_slot[i], t = base + i;
+    if (s0 < 0) continue;                             // the same for every thread
+    if (threadIdx.x == 0) run_len = B;
+    __syncthreads();
+    const int most = (int)min((int64_t)B, a.num_tokens - t);
+    for (int k = threadIdx.x; k < B; k += kRotThreads)
+      if (k >= most || a.slots[t + k] != s0 + k) atomicMin(&run_len, k);
+    __syncthreads();
+    const int n = run_len;
+    const int64_t blk = s0 / B;
+    for (int h0 = 0; h0 < a.num_kv_heads; h0 += WARPS * kHeadsPerWarp) {
+      float ka[kHeadsPerWarp] = {}, va[kHeadsPerWarp] = {};
+      for (int r0 = 0; r0 < n; r0 += kRunTokens) {
+        const int nt = min(kRunTokens, n - r0);
+        __syncthreads();                              // cs of the last round is used up
+        for (int x = threadIdx.x; x < nt * half; x += kRotThreads) {
+          const int tk = x / half, p = x - tk * half;
+          cs[tk][p] = cos_sin(a.positions[axis[p] * a.position_stride + t + r0 + tk], turn[p]);
+        }
+        __syncthreads();
+        if (lane_row >= rows_at_once) continue;       // joins the barriers above again
 #pragma unroll
-      for (int j = 0; j < kMaxPairs; ++j) {
-        const int p = lane + 32 * j;
-        if (p >= half) break;
-        float x, y;
-        rotate(static_cast<float>(k[INTER ? 2 * p : p]),
-               static_cast<float>(k[INTER ? 2 * p + 1 : p + half]),
-               cos_sin(a.positions[axis[j] * a.position_stride + t + r], turn[j]), x, y);
-        ka = fmaxf(ka, fmaxf(fabsf(x), fabsf(y)));
+        for (int q = 0; q < kHeadsPerWarp; ++q) {
+          const int h = h0 + q * WARPS + warp;
+          if (h >= a.num_kv_heads) break;
+#pragma unroll 4
+          for (int tk = lane_row; tk < nt; tk += rows_at_once) {
+            const T* k = (const T*)a.k + (t + r0 + tk) * a.k_stride + (int64_t)h * D;
+            const T* v = (const T*)a.v + (t + r0 + tk) * a.v_stride + (int64_t)h * D;
+            float x[2 * N], y[2 * N];
+            Vec<T>::to_f32(*reinterpret_cast<const uint4*>(k + e0), x);
+            Vec<T>::to_f32(*reinterpret_cast<const uint4*>(k + e1), x + N);
+            Vec<T>::to_f32(*reinterpret_cast<const uint4*>(v + e0), y);
+            Vec<T>::to_f32(*reinterpret_cast<const uint4*>(v + e1), y + N);
+            if (rot) {
+#pragma unroll
+              for (int e = 0; e < N; ++e) {
+                const float2 w = cs[tk][c * N + e];
+                if (INTER) rotate(x[2 * e], x[2 * e + 1], w, x[2 * e], x[2 * e + 1]);
+                else rotate(x[e], x[N + e], w, x[e], x[N + e]);
+              }
+            }
+            // fmaxf leaves a NaN out
+#pragma unroll
+            for (int e = 0; e < 2 * N; ++e) {
+              ka[q] = fmaxf(ka[q], fabsf(x[e]));
+              va[q] = fmaxf(va[q], fabsf(y[e]));
+            }
+          }
+        }
       }
-      for (int e = a.rot_size + lane; e < D; e += 32) ka = fmaxf(ka, fabsf(static_cast<float>(k[e])));
-      for (int e = lane; e < D; e += 32) va = fmaxf(va, fabsf(static_cast<float>(v[e])));
-    }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      ka = fmaxf(ka, __shfl_xor_sync(0xffffffffu, ka, o));
-      va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, o));
-    }
-    if (lane == 0) {
-      const int64_t idx = (s0 / a.block_size) * a.num_kv_heads + h;
-      a.k_scales[idx] = block_scale_of(ka);
-      a.v_scales[idx] = block_scale_of(va);
+      for (int q = 0; q < kHeadsPerWarp; ++q) {
+        const int h = h0 + q * WARPS + warp;
+        if (h >= a.num_kv_heads) break;               // the same for the whole warp
+        float km = ka[q], vm = va[q];
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) {
+          km = fmaxf(km, __shfl_xor_sync(0xffffffffu, km, o));
+          vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
+        }
+        if (lane == 0) {
+          a.k_scales[blk * a.num_kv_heads + h] = block_scale_of(km);
+          a.v_scales[blk * a.num_kv_heads + h] = block_scale_of(vm);
+        }
+      }
     }
   }
 }
 
-template <typename T, bool FP8, bool INTER>
+template <typename T, int POOL, bool INTER>
 cudaError_t launch_rotary_t(const RotaryArgs& a, int sm_count, cudaStream_t st) {
-  if (FP8 && a.k_scales != nullptr) {
-    const int64_t warps = a.num_tokens * a.num_kv_heads;
-    int64_t blocks = (warps + kRotThreads / 32 - 1) / (kRotThreads / 32);
-    if (blocks > (int64_t)sm_count * 16) blocks = (int64_t)sm_count * 16;
+  if (POOL == 2) {
+    const int64_t blocks = (a.num_tokens + kScaleTokens - 1) / kScaleTokens;
+    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const cudaError_t e = launch_pdl(rotary_scales_kernel<T, INTER>, dim3((unsigned)blocks),
                                      dim3(kRotThreads), 0, st, a);
     if (e != cudaSuccess) return e;
   }
-  // few tokens: one per CTA, so that they spread over the SMs; many: four
-  // per CTA, which share a round's barriers
-  if (a.num_tokens <= (int64_t)sm_count * 8)
-    return launch_pdl(rotary_kernel<T, FP8, INTER, 1>, dim3((unsigned)a.num_tokens),
-                      dim3(kRotThreads), 0, st, a);
-  int64_t blocks = (a.num_tokens + 3) / 4;
-  if (blocks > 0x7fffffffll) blocks = 0x7fffffffll;
-  return launch_pdl(rotary_kernel<T, FP8, INTER, 4>, dim3((unsigned)blocks), dim3(kRotThreads), 0,
-                    st, a);
+  // few tokens: one per CTA, so that they spread over the SMs; more: two or
+  // four per CTA, which share a round's barriers, as long as that leaves
+  // several waves of CTAs (some five are resident per SM)
+  auto go = [&](auto kernel, int tok) {
+    const int64_t blocks = std::min<int64_t>((a.num_tokens + tok - 1) / tok, 0x7fffffffll);
+    return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRotThreads), 0, st, a);
+  };
+  if (a.num_tokens <= (int64_t)sm_count * 8) return go(rotary_kernel<T, POOL, INTER, 1>, 1);
+  if (a.num_tokens <= (int64_t)sm_count * 80) return go(rotary_kernel<T, POOL, INTER, 2>, 2);
+  return go(rotary_kernel<T, POOL, INTER, 4>, 4);
+}
+
+template <typename T, int POOL>
+cudaError_t launch_rotary_i(const RotaryArgs& a, int sm_count, cudaStream_t st) {
+  return a.interleaved ? launch_rotary_t<T, POOL, true>(a, sm_count, st)
+                       : launch_rotary_t<T, POOL, false>(a, sm_count, st);
 }
 
 template <typename T>
 cudaError_t launch_rotary_d(const RotaryArgs& a, int sm_count, cudaStream_t st) {
-  if (a.pool == 1)
-    return a.interleaved ? launch_rotary_t<T, true, true>(a, sm_count, st)
-                         : launch_rotary_t<T, true, false>(a, sm_count, st);
-  return a.interleaved ? launch_rotary_t<T, false, true>(a, sm_count, st)
-                       : launch_rotary_t<T, false, false>(a, sm_count, st);
+  if (a.pool == 0) return launch_rotary_i<T, 0>(a, sm_count, st);
+  return a.k_scales == nullptr ? launch_rotary_i<T, 1>(a, sm_count, st)
+                               : launch_rotary_i<T, 2>(a, sm_count, st);
 }
 
 }  // namespace

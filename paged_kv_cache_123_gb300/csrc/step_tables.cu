@@ -36,6 +36,11 @@ namespace {
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 constexpr int kPlanMaxCluster = 8;
+constexpr int kFillThreads = 512;
+constexpr int kFillGroups = 4;    // 64-row groups a warp takes at a time
+constexpr int kAtOnce = 16;       // table entries a lane has in flight
+// requests whose query_start_loc is staged in shared memory for the searches
+constexpr int kStagedSeqs = 12 * 1024 - 1;
 
 struct Sum2 {
   int64_t a, b;
@@ -125,48 +130,124 @@ __device__ __forceinline__ Sum2 request_need(const ExtendArgs& a, int r) {
   return Sum2{n, (int64_t)need - held};
 }
 
-// Token rows first, first + step, ...: position, slot, and the table entry
-// of each block that a row opens. Rows behind the last token are padding
-// (position 0, slot -1). `head` is the ring head before this step.
-__device__ __forceinline__ void fill_tokens(const ExtendArgs& a, int64_t head, int64_t first,
-                                            int64_t step) {
-  const int64_t total = a.query_start_loc[a.num_seqs];
-  const int64_t base = a.ring_size > 0 ? head % a.ring_size : 0;
+// Last request in [lo, hi) that starts at or before row t (query_start_loc[lo]
+// <= t).
+__device__ __forceinline__ int request_of(const int32_t* qsl, int64_t t, int lo, int hi) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)qsl[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// p / B, by a shift where B is a power of two (shift >= 0)
+__device__ __forceinline__ uint32_t block_of(uint32_t p, uint32_t B, int shift) {
+  return shift >= 0 ? p >> shift : p / B;
+}
+
+// Where token row t of request r goes: its position, and the entry (of the
+// table, or of the ring when it opens or continues a new block) that names
+// its block.
+struct RowPlace {
+  int64_t pos;
+  uint32_t row;
+  const int32_t* src;
+  int32_t* opens;            // table entry to write, or nullptr
+};
+__device__ __forceinline__ RowPlace place_row(const ExtendArgs& a, const int32_t* qsl, int r,
+                                              int64_t t, int64_t base, int shift) {
   const uint32_t B = (uint32_t)a.block_size;
-  for (int64_t t = first; t < a.num_tokens; t += step) {
-    int64_t pos = 0, slot = -1;
-    if (t < total) {
-      int lo = 0, hi = a.num_seqs;          // last request that starts at or before t
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)a.query_start_loc[mid] <= t) lo = mid; else hi = mid;
-      }
-      const int64_t q0 = a.query_start_loc[lo];
-      const int n = (int)(a.query_start_loc[lo + 1] - q0);
-      const uint32_t ctx = (uint32_t)(a.seq_lens[lo] - n);
-      const uint32_t p = ctx + (uint32_t)(t - q0);
-      const uint32_t lb = p / B, row = p - lb * B;
-      const uint32_t held = (ctx + (B - 1)) / B;
-      int32_t* entry = a.block_tables + (int64_t)lo * a.table_stride + lb;
-      int64_t blk;
-      if (lb < held) {
-        blk = *entry;
-      } else {
-        blk = a.free_ring[ring_at(base, a.block_start_loc[lo] + (int64_t)(lb - held),
-                                  a.ring_size)];
-        if (row == 0) *entry = (int32_t)blk;
-      }
-      pos = p;
-      if (blk < 0 || blk >= a.num_blocks) latch(a.err, PA_ERR_OUT_OF_RANGE);
-      else slot = blk * B + row;
+  const int64_t q0 = qsl[r];
+  const int n = (int)(qsl[r + 1] - q0);
+  const uint32_t ctx = (uint32_t)(a.seq_lens[r] - n);
+  const uint32_t p = ctx + (uint32_t)(t - q0);
+  const uint32_t lb = block_of(p, B, shift);
+  const uint32_t held = block_of(ctx + (B - 1), B, shift);
+  int32_t* entry = a.block_tables + (int64_t)r * a.table_stride + lb;
+  RowPlace w;
+  w.pos = p;
+  w.row = p - lb * B;
+  w.src = lb < held ? entry
+                    : a.free_ring + ring_at(base, a.block_start_loc[r] + (int64_t)(lb - held),
+                                            a.ring_size);
+  w.opens = lb >= held && w.row == 0 ? entry : nullptr;
+  return w;
+}
+__device__ __forceinline__ int64_t slot_of(const ExtendArgs& a, const RowPlace& w, int32_t blk) {
+  if (w.opens != nullptr) *w.opens = blk;
+  if (blk < 0 || blk >= a.num_blocks) {
+    latch(a.err, PA_ERR_OUT_OF_RANGE);
+    return -1;
+  }
+  return (int64_t)blk * a.block_size + w.row;
+}
+
+// Token rows: warp `first` of `step` takes `groups` x 64 consecutive rows at a
+// time, a lane two of each 64. The requests of the warp's first and last row
+// are searched once (every lane the same loads); a lane then searches between
+// them, which for prompts is next to no search. Rows behind the last token are
+// padding (position 0, slot -1). `qsl` is query_start_loc or a copy in shared
+// memory, `head` the ring head before this step.
+__device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* qsl, int64_t head,
+                                            int64_t first, int64_t step, int groups) {
+  const int lane = threadIdx.x & 31;
+  const int64_t total = qsl[a.num_seqs];
+  const int64_t base = a.ring_size > 0 ? head % a.ring_size : 0;
+  const int shift = (a.block_size & (a.block_size - 1)) == 0 ? __ffs(a.block_size) - 1 : -1;
+  const bool pairs = (reinterpret_cast<uintptr_t>(a.positions) & 15) == 0 &&
+                     (reinterpret_cast<uintptr_t>(a.slot_mapping) & 15) == 0;
+  const int64_t span = 64 * (int64_t)groups;
+  for (int64_t t0 = first * span; t0 < a.num_tokens; t0 += step * span) {
+    int lo = 0, hi = a.num_seqs;
+    if (t0 < total) {
+      lo = request_of(qsl, t0, 0, a.num_seqs);
+      hi = request_of(qsl, min(t0 + span, total) - 1, lo, a.num_seqs) + 1;
     }
-    a.positions[t] = pos;
-    a.slot_mapping[t] = slot;
+#pragma unroll 2
+    for (int g = 0; g < groups; ++g) {
+      const int64_t t = t0 + 64 * g + 2 * lane;
+      longlong2 pos = make_longlong2(0, 0), slot = make_longlong2(-1, -1);
+      if (t < total) {
+        // both rows' loads before either's stores
+        const int r = request_of(qsl, t, lo, hi);
+        const RowPlace w0 = place_row(a, qsl, r, t, base, shift);
+        const bool two = t + 1 < total;
+        RowPlace w1 = w0;
+        if (two)
+          w1 = place_row(a, qsl, (int64_t)qsl[r + 1] <= t + 1 ? request_of(qsl, t + 1, r, hi) : r,
+                         t + 1, base, shift);
+        const int32_t b0 = *w0.src, b1 = *w1.src;
+        pos.x = w0.pos;
+        slot.x = slot_of(a, w0, b0);
+        if (two) {
+          pos.y = w1.pos;
+          slot.y = slot_of(a, w1, b1);
+        }
+      }
+      if (pairs && t + 1 < a.num_tokens) {
+        *reinterpret_cast<longlong2*>(a.positions + t) = pos;
+        *reinterpret_cast<longlong2*>(a.slot_mapping + t) = slot;
+      } else {
+        if (t < a.num_tokens) { a.positions[t] = pos.x; a.slot_mapping[t] = slot.x; }
+        if (t + 1 < a.num_tokens) { a.positions[t + 1] = pos.y; a.slot_mapping[t + 1] = slot.y; }
+      }
+    }
   }
 }
 
+// query_start_loc in shared memory, if it fits: the searches are chains of
+// dependent loads.
+__device__ __forceinline__ const int32_t* stage_starts(const ExtendArgs& a, int32_t* staged) {
+  if (a.num_seqs > kStagedSeqs) return a.query_start_loc;
+  for (int i = threadIdx.x; i <= a.num_seqs; i += blockDim.x) staged[i] = a.query_start_loc[i];
+  __syncthreads();
+  return staged;
+}
+int staged_bytes(int num_seqs) { return num_seqs > kStagedSeqs ? 0 : (num_seqs + 1) * 4; }
+
 template <bool FUSED>
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendArgs a) {
+  extern __shared__ int32_t staged[];
   __shared__ Sum2 warp_sums[kPlanWarps];
   __shared__ Sum2 slot;
   cg::cluster_group cl = cg::this_cluster();
@@ -224,16 +305,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
   if (FUSED) __threadfence();
   cl.sync();            // shared memory of this CTA is no longer read; FUSED: sums visible
   if (FUSED)
-    fill_tokens(a, head, (int64_t)rank * kPlanThreads + threadIdx.x,
-                (int64_t)count * kPlanThreads);
+    fill_tokens(a, stage_starts(a, staged), head,
+                (int64_t)rank * kPlanWarps + (threadIdx.x >> 5), (int64_t)count * kPlanWarps, 1);
 }
 
-__global__ void __launch_bounds__(256) extend_fill_kernel(const ExtendArgs a) {
+__global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(const ExtendArgs a) {
+  extern __shared__ int32_t staged[];
   griddep_launch();
   griddep_wait();
   const int64_t head = a.ring_state_out[0] - a.block_start_loc[a.num_seqs];
-  fill_tokens(a, head, (int64_t)blockIdx.x * blockDim.x + threadIdx.x,
-              (int64_t)gridDim.x * blockDim.x);
+  fill_tokens(a, stage_starts(a, staged), head, (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5),
+              (int64_t)gridDim.x * (blockDim.x >> 5), kFillGroups);
 }
 
 // Table entries that request r holds, 0 if it is not finished; a length
@@ -260,10 +342,18 @@ __device__ __forceinline__ void count_rows(const ReleaseArgs& a, int first, int 
     const int n = held_entries(a, r);
     const int32_t* row = a.block_tables + (int64_t)r * a.table_stride;
     int c = 0;
-    for (int j = lane; j < n; j += 32) {
-      const int32_t id = row[j];
-      if (is_block(a, id)) ++c;
-      else if (id >= 0) latch(a.err, PA_ERR_OUT_OF_RANGE);
+    for (int j0 = 0; j0 < n; j0 += 32 * kAtOnce) {
+      int32_t id[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int j = j0 + 32 * k + lane;
+        id[k] = j < n ? row[j] : -1;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        if (is_block(a, id[k])) ++c;
+        else if (id[k] >= 0) latch(a.err, PA_ERR_OUT_OF_RANGE);
+      }
     }
     c = __reduce_add_sync(0xffffffffu, c);
     if (lane == 0) a.release_start_loc[r + 1] = c;
@@ -321,14 +411,21 @@ __device__ __forceinline__ void return_rows(const ReleaseArgs& a, int first, int
     if (n > 0) {
       const int32_t* row = a.block_tables + (int64_t)r * a.table_stride;
       int done = 0;
-      for (int j0 = 0; done < n; j0 += 32) {
-        const int32_t id = j0 + lane < a.table_stride ? row[j0 + lane] : -1;
-        const unsigned m = __ballot_sync(0xffffffffu, is_block(a, id));
-        const int k = done + __popc(m & ((1u << lane) - 1u));
-        if (((m >> lane) & 1u) && k < n)
-          a.free_ring[ring_at(base, at + k, a.ring_size)] = id;
-        done += __popc(m);
-        if (j0 + 32 >= a.table_stride) break;
+      for (int64_t j0 = 0; done < n && j0 < a.table_stride; j0 += 32 * kAtOnce) {
+        int32_t id[kAtOnce];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const int64_t j = j0 + 32 * k + lane;
+          id[k] = j < a.table_stride ? row[j] : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const bool mine = is_block(a, id[k]);
+          const unsigned m = __ballot_sync(0xffffffffu, mine);
+          const int x = done + __popc(m & ((1u << lane) - 1u));
+          if (mine && x < n) a.free_ring[ring_at(base, at + x, a.ring_size)] = id[k];
+          done += __popc(m);
+        }
       }
     }
   }
@@ -375,8 +472,10 @@ __global__ void __launch_bounds__(256) release_return_kernel(const ReleaseArgs a
 }
 
 template <typename Args>
-cudaError_t launch_cluster(void (*kernel)(Args), int ctas, cudaStream_t st, const Args& a) {
+cudaError_t launch_cluster(void (*kernel)(Args), int ctas, size_t smem, cudaStream_t st,
+                           const Args& a) {
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = smem;
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = st;
@@ -399,34 +498,36 @@ int cluster_for(int64_t threads) {
 
 // token rows that the cluster itself fills; table entries that it returns
 constexpr int64_t kFusedTokens = 4 * kPlanMaxCluster * kPlanThreads;
-constexpr int64_t kFusedEntries = 64 * 1024;
+constexpr int64_t kFusedEntries = 256 * 1024;
 
 }  // namespace
 
 cudaError_t launch_extend_tables(const ExtendArgs& a, int sm_count, cudaStream_t st) {
   if (a.num_tokens <= kFusedTokens)
     return launch_cluster(extend_plan_kernel<true>,
-                          cluster_for(a.num_tokens > a.num_seqs ? a.num_tokens : a.num_seqs), st,
-                          a);
+                          cluster_for(a.num_tokens > a.num_seqs ? a.num_tokens : a.num_seqs),
+                          staged_bytes(a.num_seqs), st, a);
   cudaError_t e =
-      launch_cluster(extend_plan_kernel<false>, cluster_for(a.num_seqs), st, a);
+      launch_cluster(extend_plan_kernel<false>, cluster_for(a.num_seqs), 0, st, a);
   if (e != cudaSuccess) return e;
-  const int threads = 256;
-  int64_t blocks = (a.num_tokens + threads - 1) / threads;
-  if (blocks > (int64_t)sm_count * 8) blocks = (int64_t)sm_count * 8;
-  return launch_pdl(extend_fill_kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
+  // two CTAs per SM at most: each stages the start rows once
+  const int rows = kFillThreads / 32 * 64 * kFillGroups;
+  int64_t blocks = (a.num_tokens + rows - 1) / rows;
+  if (blocks > (int64_t)sm_count * 2) blocks = (int64_t)sm_count * 2;
+  return launch_pdl(extend_fill_kernel, dim3((unsigned)blocks), dim3(kFillThreads),
+                    (size_t)staged_bytes(a.num_seqs), st, a);
 }
 
 cudaError_t launch_release_tables(const ReleaseArgs& a, int sm_count, cudaStream_t st) {
   if ((int64_t)a.num_seqs * a.table_stride <= kFusedEntries)
-    return launch_cluster(release_one_kernel, cluster_for((int64_t)a.num_seqs * 32), st, a);
+    return launch_cluster(release_one_kernel, cluster_for((int64_t)a.num_seqs * 32), 0, st, a);
   const int threads = 256, rows = threads / 32;
   int64_t blocks = ((int64_t)a.num_seqs + rows - 1) / rows;
   if (blocks > (int64_t)sm_count * 8) blocks = (int64_t)sm_count * 8;
   cudaError_t e =
       launch_pdl(release_count_kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
   if (e != cudaSuccess) return e;
-  e = launch_cluster(release_scan_kernel, cluster_for(a.num_seqs), st, a);
+  e = launch_cluster(release_scan_kernel, cluster_for(a.num_seqs), 0, st, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(release_return_kernel, dim3((unsigned)blocks), dim3(threads), 0, st, a);
 }
