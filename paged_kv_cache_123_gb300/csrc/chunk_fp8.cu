@@ -19,9 +19,8 @@
 // its row tile and takes every key tile (a key tile is loaded and widened
 // once for 256 rows); with fewer, both have the same rows and take the key
 // tiles in turn, and their results meet at the end.
-//   * a producer warp brings the tiles' codes (K and V in the order in which
-//     the MMAs need them) by 3-D TMA boxes, one per block piece, into a ring
-//     of raw stages;
+//   * two producer warps bring the tiles' codes (K and V) by 3-D TMA boxes,
+//     one per block piece, into a ring of raw stages;
 //   * four converter warps widen each raw tile to fp16 (E4M3 is exact in
 //     fp16) into the 128-byte-swizzled operand layout of the MMA, two stages
 //     each of K and V, and clear rows without a token on the way;
@@ -65,7 +64,7 @@ namespace {
 constexpr int kRows = 128;                // rows of a chain (MMA M)
 constexpr int kKv = 128;                  // KV tokens per tile
 constexpr int kMmaWarp = 0;
-constexpr int kProducerWarp = 1;
+constexpr int kProducerWarp = 1;          // K, and 2: V
 constexpr int kConvWarp = 4;              // 4-7: converters
 constexpr int kConvWarps = 4;
 constexpr int kSoftmaxWarp = 8;           // 8-11, 12-15: the chains' softmax
@@ -185,19 +184,8 @@ __device__ __forceinline__ bool lengths_ok(const ChunkArgs& a, int q0, int n, in
          (int64_t)q0 + n <= a.num_tokens && (int64_t)L <= a.table_stride * a.block_size;
 }
 
-// Order of the raw tiles: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1), as the
-// MMAs consume them. Item `it` of 2n: true for V, *j its tile.
-__device__ __forceinline__ bool item_of(int it, int n, int* j) {
-  if (it == 0) { *j = 0; return false; }
-  if (it & 1) {
-    *j = (it + 1) >> 1;
-    if (*j < n) return false;
-    *j = n - 1;
-    return true;
-  }
-  *j = (it - 2) >> 1;
-  return true;
-}
+// Order of the raw tiles: K0 V0 K1 V1 ..., so that a V never waits behind a K
+// whose place the scores still use. Item `it` of 2n: V if odd, tile it / 2.
 
 // Table entry of this lane's block piece of tile t (-1: none, or a piece
 // that no row's window reaches, which is never looked up).
@@ -213,34 +201,24 @@ struct Pieces {
   }
 };
 
+// Producer warp of K (items 0, 2, ...) or V (1, 3, ...): lane p loads piece p
+// of a tile. One warp each: a box costs its lane some 90 clocks to issue, and
+// a tile of 16-token blocks has eight.
 template <int D>
-__device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtensorMap* tmV,
-                        const Pieces& pc, int kvh, uint32_t tiles, uint32_t bar,
-                        volatile uint32_t* masks, volatile int* abort_flag, int raw_log2,
-                        int lane) {
+__device__ void produce(const ChunkArgs& a, const CUtensorMap* tm, bool isv, const Pieces& pc,
+                        int kvh, uint32_t tiles, uint32_t bar, volatile uint32_t* masks,
+                        volatile int* abort_flag, int raw_log2, int lane) {
   using Ly = ChunkLayout<D>;
-  if (lane == 0) {
-    prefetch_tensormap(tmK);
-    prefetch_tensormap(tmV);
-  }
+  if (lane == 0) prefetch_tensormap(tm);
   const int n = pc.ntiles, nraw = 1 << raw_log2;
-  // entries of the K tile to come and of the one behind it are read ahead;
-  // the two K tiles gone by are kept for their V
-  int e0 = pc.entry(0, lane), e1 = pc.entry(1, lane), h0 = -1, h1 = -1;
+  // entries of this tile and the next are read ahead
+  int e0 = pc.entry(0, lane), e1 = pc.entry(1, lane);
   int issued = 0;
-  for (int it = 0; it < 2 * n; ++it) {
-    int j;
-    const bool isv = item_of(it, n, &j);
-    int ent;
-    if (!isv) {
-      ent = e0;
-      h1 = h0;
-      h0 = e0;
-      e0 = e1;
-      e1 = pc.entry(j + 2, lane);
-    } else {
-      ent = j == n - 1 ? h0 : h1;
-    }
+  for (int j = 0; j < n; ++j) {
+    const int it = 2 * j + (isv ? 1 : 0);
+    const int ent = e0;
+    e0 = e1;
+    e1 = pc.entry(j + 2, lane);
     const int ts = pc.kv_lo + j * kKv;
     const int tok = ts + lane * pc.R;
     const bool mine = ent >= 0 && ent < a.num_blocks;
@@ -263,15 +241,19 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tmK, const CUtens
     ok = __shfl_sync(0xffffffffu, ok, 0);
     if (!ok) break;
     if (mine)
-      tma_load_3d(tiles + Ly::RAW_OFF + st * Ly::RAW + lane * pc.R * D, isv ? tmV : tmK, 0,
+      tma_load_3d(tiles + Ly::RAW_OFF + st * Ly::RAW + lane * pc.R * D, tm, 0,
                   tok & (a.block_size - 1), (int)((int64_t)ent * a.num_kv_heads + kvh),
                   bar + 8u * (kRawFull + st));
-    issued = it + 1;
+    issued = j + 1;
   }
-  // this warp's copies land before the CTA can leave, also after a timeout
+  // this warp's copies land before the CTA can leave, also after a timeout: the
+  // last item of each of its nraw / 2 stages (an older one's phase is over)
   if (lane == 0)
-    for (int i = issued > nraw ? issued - nraw : 0; i < issued; ++i)
-      mbar_wait_drain(bar + 8u * (kRawFull + (i & (nraw - 1))), (i >> raw_log2) & 1, kWaitCycles);
+    for (int j = max(0, issued - nraw / 2); j < issued; ++j) {
+      const int it = 2 * j + (isv ? 1 : 0);
+      mbar_wait_drain(bar + 8u * (kRawFull + (it & (nraw - 1))), (it >> raw_log2) & 1,
+                      kWaitCycles);
+    }
 }
 
 // Q rows of a tile to fp16, each divided by the power of two of its largest
@@ -401,21 +383,25 @@ struct ConvLane {
 };
 static_assert(ConvLane<128>::ROWS % 8 == 0 && ConvLane<64>::ROWS % 8 == 0, "swizzle period");
 
-// Raw tile -> fp16 operand tile. Rows without a token become zero. clean:
-// NaN codes become zero; returns whether this lane met any.
+// Raw tile -> fp16 operand tile, through registers, so that the raw stage is
+// free as soon as it is read. Rows without a token become zero. clean: NaN
+// codes become zero; returns whether this lane met any.
 template <int D>
-__device__ __forceinline__ bool convert_tile(const ConvLane<D>& ln, uint32_t raw, uint32_t dst,
+__device__ __forceinline__ void load_raw(const ConvLane<D>& ln, uint32_t raw,
+                                         uint32_t (&w)[ConvLane<D>::STEPS][4]) {
+#pragma unroll
+  for (int s = 0; s < ConvLane<D>::STEPS; ++s)
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[s][0]), "=r"(w[s][1]), "=r"(w[s][2]), "=r"(w[s][3])
+                 : "r"(raw + ln.src + s * ConvLane<D>::ROWS * D) : "memory");
+}
+template <int D>
+__device__ __forceinline__ bool convert_tile(const ConvLane<D>& ln,
+                                             uint32_t (&w)[ConvLane<D>::STEPS][4], uint32_t dst,
                                              bool whole, int rows, unsigned pm, int rshift,
                                              bool clean) {
   using CL = ConvLane<D>;
   bool seen = false;
-  // all loads first: their latency is paid once
-  uint32_t w[CL::STEPS][4];
-#pragma unroll
-  for (int s = 0; s < CL::STEPS; ++s)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(w[s][0]), "=r"(w[s][1]), "=r"(w[s][2]), "=r"(w[s][3])
-                 : "r"(raw + ln.src + s * CL::ROWS * D));
   if (!whole) {
 #pragma unroll
     for (int s = 0; s < CL::STEPS; ++s) {
@@ -642,8 +628,10 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   const int lo_last = a.window > 0 ? max(0, L - n + sp.i_last + 1 - a.window) : 0;
 
   if (warp < kSoftmaxWarp) {
-    if (warp == kProducerWarp) {
-      produce<D>(a, &tmK, &tmV, pc, kvh, tiles, bar, masks, abort_flag, raw_log2, lane);
+    if (warp == kProducerWarp || warp == kProducerWarp + 1) {
+      const bool isv = warp > kProducerWarp;
+      produce<D>(a, isv ? &tmV : &tmK, isv, pc, kvh, tiles, bar, masks, abort_flag, raw_log2,
+                 lane);
     } else if (warp == kMmaWarp) {
       if (tmem != 0) *abort_flag = 1;
       else if (alt) issue<D, true>(ntiles, tiles, bar, abort_flag);
@@ -653,28 +641,31 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       const int cw = warp - kConvWarp;
       const ConvLane<D> ln(cw, lane);
       for (int it = 0; it < 2 * ntiles; ++it) {
-        int j;
-        const bool isv = item_of(it, ntiles, &j);
+        const int j = it >> 1;
+        const bool isv = (it & 1) != 0;
         const int rs = it & (nraw - 1), st = j & 1;
         bool ok = mbar_wait_bounded(bar + 8u * (kRawFull + rs), (it >> raw_log2) & 1, abort_flag,
                                     kWaitCycles);
-        if (ok && j >= 2)
+        if (!__all_sync(0xffffffffu, ok)) break;
+        const unsigned pm = masks[rs];
+        uint32_t w[ConvLane<D>::STEPS][4];
+        load_raw<D>(ln, tiles + Ly::RAW_OFF + rs * Ly::RAW, w);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar + 8u * (kRawEmpty + rs));
+        if (j >= 2)
           ok = mbar_wait_bounded(bar + 8u * ((isv ? kVEmpty : kKEmpty) + st), ((j >> 1) - 1) & 1,
                                  abort_flag, kWaitCycles);
         if (!__all_sync(0xffffffffu, ok)) break;
         const int ts = kv_lo + j * kKv;
         const int rows = min(kKv, kv_end - ts);
-        const unsigned pm = masks[rs];
         const bool clean = isv && (ts + kKv - 1 > pos_first || ts < lo_last);
-        const bool seen = convert_tile<D>(
-            ln, tiles + Ly::RAW_OFF + rs * Ly::RAW,
-            tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE,
-            pm == full_mask && rows == kKv, rows, pm, rshift, clean);
+        const bool seen =
+            convert_tile<D>(ln, w, tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE,
+                            pm == full_mask && rows == kKv, rows, pm, rshift, clean);
         if (seen) misc[6] = 1;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar + 8u * (kRawEmpty + rs));
           mbar_arrive(bar + 8u * ((isv ? kVFull : kKFull) + st));
         }
       }
