@@ -90,8 +90,10 @@ struct ChunkLayout {
   // small things first, so that the 1024-byte aligned tiles end exactly at
   // the limit of 227 KB for head size 128
   static constexpr int BAR_OFF = 0;
-  static constexpr int MISC_OFF = (kBars * 8 + 15) / 16 * 16;   // tmem base, abort, masks, NaN
-  static constexpr int ROW_OFF = MISC_OFF + 32;                 // float [2][128] Q row factors
+  // words: 0 tmem base, 1 abort flag, 2-5 piece masks of the raw stages, 6
+  // NaN codes met, 8-11 piece masks of the last four K tiles
+  static constexpr int MISC_OFF = (kBars * 8 + 15) / 16 * 16;
+  static constexpr int ROW_OFF = MISC_OFF + 64;                 // float [2][128] Q row factors
   static constexpr int ML_OFF = ROW_OFF + 2 * kRows * 4;        // float [2][128] second chain's m, l
   static constexpr int SMALL = ML_OFF + 2 * kRows * 4;
   static constexpr int HALVES = D / 64;
@@ -548,6 +550,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem_raw + Ly::MISC_OFF);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem_raw + Ly::MISC_OFF + 4);
   volatile uint32_t* masks = misc + 2;
+  volatile uint32_t* tile_mask = misc + 8;
   float* row_factor = reinterpret_cast<float*>(smem_raw + Ly::ROW_OFF);   // [2][128]
   float* second_ml = reinterpret_cast<float*>(smem_raw + Ly::ML_OFF);     // [2][128]
   if (tiles + Ly::TILES > sbase + Ly::SMEM) {       // base too far off 1024 bytes
@@ -663,6 +666,9 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             convert_tile<D>(ln, w, tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE,
                             pm == full_mask && rows == kKv, rows, pm, rshift, clean);
         if (seen) misc[6] = 1;
+        // (a slot is used again four tiles on, when S of the tile two on, and
+        // so the softmax of this one, is long over)
+        if (!isv && cw == 0 && lane == 0) tile_mask[j & 3] = pm;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -701,9 +707,12 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     const float f0 = (a.scale == 0.f ? 1.f : fabsf(a.scale)) * kLog2e *
                      (SCALED ? 1.f : a.k_scale) * row_factor[(alt ? 0 : c * kRows) + r];
 
-    // this chain's tiles: j = j0, j0 + dj, ...
+    // this chain's tiles: j = j0, j0 + dj, ...; those that begin at fast_lo or
+    // later and end by fast_hi are seen whole by every row of the warp
     const int j0 = alt ? c : 0, dj = alt ? 2 : 1;
-    int ent = pc.entry(j0, lane), ent_next = pc.entry(j0 + dj, lane);
+    const int fast_lo = __reduce_max_sync(0xffffffffu, rv ? lo : 0);
+    const int fast_hi = __reduce_min_sync(0xffffffffu, rv ? pos + 1 : 0x7fffffff);
+    int ent_next = SCALED ? pc.entry(j0, lane) : -1;
     float ksl = 1.f, vsl = 0.f;                       // scales of this lane's piece
     auto load_scales = [&](int e, float& k, float& v) {
       k = 1.f;
@@ -713,22 +722,21 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         v = a.v_scales[(int64_t)e * a.num_kv_heads + kvh];
       }
     };
-    load_scales(ent, ksl, vsl);
+    if (SCALED) {
+      load_scales(ent_next, ksl, vsl);
+      ent_next = pc.entry(j0 + dj, lane);
+    }
     float m_use = kNegInfC, l = 0.f, vref = 0.f;
     int t = 0;
     for (int j = j0; j < ntiles; j += dj, ++t) {
       const int ts = kv_lo + j * kKv;
       const int te = min(kv_end, ts + kKv);
-      const unsigned pm = __ballot_sync(0xffffffffu, ent >= 0 && ent < a.num_blocks);
-      float ks_next, vs_next;
-      load_scales(ent_next, ks_next, vs_next);
-      const int ent_2 = pc.entry(j + 2 * dj, lane);
-      const bool whole = pm == full_mask && te - ts == kKv;
-      const int hi = min(pos, te - 1) - ts;          // last column in sight
-      const int first = lo - ts;                     // first column in sight
-      const bool fast = __all_sync(0xffffffffu, (whole && hi >= kKv - 1 && first <= 0) || !rv);
+      float ks_next = 1.f, vs_next = 0.f;
+      int ent_2 = -1;
       float alpha_v = 1.f, rcp_ref = 0.f;
       if (SCALED) {
+        load_scales(ent_next, ks_next, vs_next);
+        ent_2 = pc.entry(j + 2 * dj, lane);
         const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vsl)));
         if (top > vref) {
           if (vref > 0.f) alpha_v = vref / top;
@@ -739,16 +747,21 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
       // the tile in two steps of 64 tokens
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        if (ok)
-          ok = mbar_wait_bounded(bar + 8u * (kSFull + 2 * c + h), t & 1, abort_flag, kWaitCycles);
+        ok = mbar_wait_bounded(bar + 8u * (kSFull + 2 * c + h), t & 1, abort_flag, kWaitCycles);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (__builtin_expect(!ok, 0)) break;
         tc_fence_after();
         if (!idle) {
           uint32_t v[kHalf];
+          const unsigned pm = tile_mask[j & 3];
           tmem_ld64(sadr + h * kHalf, v);
-          if (!fast && rv) {
-            // what a row does not see becomes -inf in place: weight 0 below
+          const bool whole = pm == full_mask && te - ts == kKv;
+          // rare paths are marked as such, which keeps the common one together
+          if (__builtin_expect(!(whole && ts >= fast_lo && te <= fast_hi), 0)) {
+            // what a row does not see becomes -inf in place: weight 0 below;
+            // rows without a token keep their scores, 0
+            const int hi = rv ? min(pos, te - 1) - ts : kKv;     // last column in sight
+            const int first = rv ? lo - ts : 0;                  // first column in sight
 #pragma unroll
             for (int ch = 0; ch < kHalf / 32; ++ch) {
               const int c0 = h * kHalf + ch * 32;
@@ -834,7 +847,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
           unpair(add_pair(sum0, sum1), s0, s1);
           l = l * alpha + (s0 + s1);
           const float alpha_o = SCALED && h == 0 ? alpha * alpha_v : alpha;
-          if (t + h >= 1 && __any_sync(0xffffffffu, alpha_o != 1.f)) {
+          if (__builtin_expect(t + h >= 1 && __any_sync(0xffffffffu, alpha_o != 1.f), 0)) {
             // after the P V of the step before
             ok = mbar_wait_bounded(bar + 8u * (kODone + 2 * c + (h ^ 1)), (t - 1 + h) & 1,
                                    abort_flag, kWaitCycles);
@@ -859,10 +872,11 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         if (lane == 0) mbar_arrive(bar + 8u * (kPFull + 2 * c + h));
       }
       if (!ok) break;
-      ent = ent_next;
-      ent_next = ent_2;
-      ksl = ks_next;
-      vsl = vs_next;
+      if (SCALED) {
+        ent_next = ent_2;
+        ksl = ks_next;
+        vsl = vs_next;
+      }
     }
     if (ok) ok = mbar_wait_bounded(bar + 8u * kDone, 0, abort_flag, kWaitCycles);
     if (ok) ok = mbar_wait_bounded(bar + 8u * kConvDone, 0, abort_flag, kWaitCycles);
