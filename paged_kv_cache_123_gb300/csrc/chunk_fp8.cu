@@ -35,11 +35,13 @@
 // fp16 products for both query types: weights are rounded to 11 bits, one
 // rounding, in [0, 2^8].
 //
-// Per-block scales: a K scale multiplies the scores of its block's columns
-// in fp32; a V scale relative to the largest one seen so far (at most 1)
-// multiplies the weights before their rounding, and the output is rescaled
-// when that reference grows, so no weight overflows and none loses more than
-// with one scale equal to the reference. The sums use the unscaled weights.
+// Per-block scales: the converters multiply a block's codes by its scale over
+// a reference, at most 1: for K the tile's largest scale, which then joins
+// the logit factor, for V the largest so far, which the output is in units of
+// (it is rescaled when that reference grows). Powers of two keep this exact
+// down to 2^-15 of the reference; below, low bits go as they would with one
+// scale equal to the reference. (Factors on the scores and weights in the
+// softmax warps, where shuffles fetched them, cost 25 % of the kernel.)
 //
 // NaN codes: a masked weight is 0, but 0 x NaN is NaN inside the MMA, so a
 // NaN in V could reach rows that do not see its token. Tiles that some row
@@ -85,6 +87,16 @@ enum : int {
   kODone = kPFull + 4, kDone = kODone + 4, kQFull, kConvDone, kBars
 };
 
+// Per-block scales of a tile: pieces over the references, and the references.
+// A slot is written with the K tile's copies; the writer is at most five
+// tiles ahead of the softmax warps (two raw tiles, one in the converters'
+// registers, two operand stages).
+struct TileScales {
+  float k[16], v[16];
+  float k_ref, v_ref, unused[2];
+};
+constexpr int kScaleSlots = 8;
+
 template <int D>
 struct ChunkLayout {
   // small things first, so that the 1024-byte aligned tiles end exactly at
@@ -94,8 +106,8 @@ struct ChunkLayout {
   // NaN codes met, 8-11 piece masks of the last four K tiles
   static constexpr int MISC_OFF = (kBars * 8 + 15) / 16 * 16;
   static constexpr int ROW_OFF = MISC_OFF + 64;                 // float [2][128] Q row factors
-  static constexpr int ML_OFF = ROW_OFF + 2 * kRows * 4;        // float [2][128] second chain's m, l
-  static constexpr int SMALL = ML_OFF + 2 * kRows * 4;
+  static constexpr int SCALE_OFF = ROW_OFF + 2 * kRows * 4;     // TileScales of the last tiles
+  static constexpr int SMALL = SCALE_OFF + kScaleSlots * (int)sizeof(TileScales);
   static constexpr int HALVES = D / 64;
   static constexpr int HALF = kKv * 128;                        // 128 rows x 64 fp16
   static constexpr int TILE = HALVES * HALF;
@@ -109,6 +121,7 @@ struct ChunkLayout {
   static constexpr int SMEM = 3 * 1024 + TILES;
   static_assert(2 * RAW <= TILE, "two raw stages where Q tile 2 is");
   static_assert(kRows * D * 4 <= 2 * TILE, "the second chain's output where K is");
+  static_assert(2 * kRows * 4 <= 2 * RAW, "its maxima and sums where the raw stages are");
   static_assert(2 * kRows * D * 2 <= 2 * TILE, "the output rows where V is");
   static_assert(SMALL <= 3 * 1024 - 16, "small region");
   static_assert(SMEM <= 232448, "over the shared memory of one CTA");
@@ -135,11 +148,6 @@ __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c)
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 __device__ __forceinline__ float cex2(float x) {      // -inf gives +0
@@ -206,21 +214,35 @@ struct Pieces {
 // Producer warp of K (items 0, 2, ...) or V (1, 3, ...): lane p loads piece p
 // of a tile. One warp each: a box costs its lane some 90 clocks to issue, and
 // a tile of 16-token blocks has eight.
-template <int D>
+// SCALED: the K warp also reads the pieces' scales, a tile ahead, and writes
+// the tile's TileScales before its copies are announced.
+template <int D, bool SCALED>
 __device__ void produce(const ChunkArgs& a, const CUtensorMap* tm, bool isv, const Pieces& pc,
                         int kvh, uint32_t tiles, uint32_t bar, volatile uint32_t* masks,
-                        volatile int* abort_flag, int raw_log2, int lane) {
+                        TileScales* scales, volatile int* abort_flag, int raw_log2, int lane) {
   using Ly = ChunkLayout<D>;
   if (lane == 0) prefetch_tensormap(tm);
   const int n = pc.ntiles, nraw = 1 << raw_log2;
   // entries of this tile and the next are read ahead
   int e0 = pc.entry(0, lane), e1 = pc.entry(1, lane);
   int issued = 0;
+  const bool with_scales = SCALED && !isv;
+  float ks = 0.f, vs = 0.f, v_ref = 0.f;
+  auto load_scales = [&](int e, float& k, float& v) {
+    k = v = 0.f;
+    if (with_scales && e >= 0 && e < a.num_blocks) {
+      k = a.k_scales[(int64_t)e * a.num_kv_heads + kvh];
+      v = a.v_scales[(int64_t)e * a.num_kv_heads + kvh];
+    }
+  };
+  load_scales(e0, ks, vs);
   for (int j = 0; j < n; ++j) {
     const int it = 2 * j + (isv ? 1 : 0);
     const int ent = e0;
     e0 = e1;
     e1 = pc.entry(j + 2, lane);
+    float ks_next, vs_next;
+    load_scales(e0, ks_next, vs_next);
     const int ts = pc.kv_lo + j * kKv;
     const int tok = ts + lane * pc.R;
     const bool mine = ent >= 0 && ent < a.num_blocks;
@@ -230,10 +252,30 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tm, bool isv, con
     const unsigned pm = __ballot_sync(0xffffffffu, mine);
     const int st = it & (nraw - 1);
     int ok = 1;
+    if (lane == 0 && it >= nraw)
+      ok = mbar_wait_bounded(bar + 8u * (kRawEmpty + st), ((it >> raw_log2) - 1) & 1, abort_flag,
+                             kWaitCycles);
+    if (with_scales) {
+      // scales are positive: their bits order as they do
+      float k_ref =
+          __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mine ? ks : 0.f)));
+      v_ref = fmaxf(v_ref, __uint_as_float(__reduce_max_sync(
+                               0xffffffffu, __float_as_uint(mine ? vs : 0.f))));
+      if (!(k_ref > 0.f)) k_ref = 1.f;
+      TileScales* ts_out = scales + (j & (kScaleSlots - 1));
+      if (lane < 16) {
+        ts_out->k[lane] = ks / k_ref;
+        ts_out->v[lane] = v_ref > 0.f ? vs / v_ref : 0.f;
+      }
+      if (lane == 0) {
+        ts_out->k_ref = k_ref;
+        ts_out->v_ref = v_ref;
+      }
+      ks = ks_next;
+      vs = vs_next;
+      __syncwarp();
+    }
     if (lane == 0) {
-      if (it >= nraw)
-        ok = mbar_wait_bounded(bar + 8u * (kRawEmpty + st), ((it >> raw_log2) - 1) & 1,
-                               abort_flag, kWaitCycles);
       if (ok) {
         masks[st] = pm;
         mbar_arrive_expect_tx(bar + 8u * (kRawFull + st),
@@ -387,7 +429,8 @@ static_assert(ConvLane<128>::ROWS % 8 == 0 && ConvLane<64>::ROWS % 8 == 0, "swiz
 
 // Raw tile -> fp16 operand tile, through registers, so that the raw stage is
 // free as soon as it is read. Rows without a token become zero. clean: NaN
-// codes become zero; returns whether this lane met any.
+// codes become zero; returns whether this lane met any. SCALED: each row
+// times its piece's entry of piece_scale.
 template <int D>
 __device__ __forceinline__ void load_raw(const ConvLane<D>& ln, uint32_t raw,
                                          uint32_t (&w)[ConvLane<D>::STEPS][4]) {
@@ -397,11 +440,11 @@ __device__ __forceinline__ void load_raw(const ConvLane<D>& ln, uint32_t raw,
                  : "=r"(w[s][0]), "=r"(w[s][1]), "=r"(w[s][2]), "=r"(w[s][3])
                  : "r"(raw + ln.src + s * ConvLane<D>::ROWS * D) : "memory");
 }
-template <int D>
+template <int D, bool SCALED>
 __device__ __forceinline__ bool convert_tile(const ConvLane<D>& ln,
                                              uint32_t (&w)[ConvLane<D>::STEPS][4], uint32_t dst,
                                              bool whole, int rows, unsigned pm, int rshift,
-                                             bool clean) {
+                                             bool clean, const float* piece_scale) {
   using CL = ConvLane<D>;
   bool seen = false;
   if (!whole) {
@@ -428,6 +471,14 @@ __device__ __forceinline__ bool convert_tile(const ConvLane<D>& ln,
     uint32_t h[8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) e4m3x4_to_f16x2x2(w[s][k], h[2 * k], h[2 * k + 1]);
+    if (SCALED) {
+      const __half2 f = __float2half2_rn(piece_scale[(ln.row + s * CL::ROWS) >> rshift]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const __half2 x = __hmul2(*reinterpret_cast<__half2*>(&h[k]), f);
+        h[k] = *reinterpret_cast<const uint32_t*>(&x);
+      }
+    }
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};"
                  ::"r"(dst + ln.dst0 + s * CL::ROWS * 128), "r"(h[0]), "r"(h[1]), "r"(h[2]),
                    "r"(h[3]) : "memory");
@@ -552,7 +603,7 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   volatile uint32_t* masks = misc + 2;
   volatile uint32_t* tile_mask = misc + 8;
   float* row_factor = reinterpret_cast<float*>(smem_raw + Ly::ROW_OFF);   // [2][128]
-  float* second_ml = reinterpret_cast<float*>(smem_raw + Ly::ML_OFF);     // [2][128]
+  TileScales* scales = reinterpret_cast<TileScales*>(smem_raw + Ly::SCALE_OFF);
   if (tiles + Ly::TILES > sbase + Ly::SMEM) {       // base too far off 1024 bytes
     if (threadIdx.x == 0) latch(a.err, PA_ERR_CUDA);
     return;
@@ -633,8 +684,8 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   if (warp < kSoftmaxWarp) {
     if (warp == kProducerWarp || warp == kProducerWarp + 1) {
       const bool isv = warp > kProducerWarp;
-      produce<D>(a, isv ? &tmV : &tmK, isv, pc, kvh, tiles, bar, masks, abort_flag, raw_log2,
-                 lane);
+      produce<D, SCALED>(a, isv ? &tmV : &tmK, isv, pc, kvh, tiles, bar, masks, scales,
+                         abort_flag, raw_log2, lane);
     } else if (warp == kMmaWarp) {
       if (tmem != 0) *abort_flag = 1;
       else if (alt) issue<D, true>(ntiles, tiles, bar, abort_flag);
@@ -663,8 +714,10 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         const int rows = min(kKv, kv_end - ts);
         const bool clean = isv && (ts + kKv - 1 > pos_first || ts < lo_last);
         const bool seen =
-            convert_tile<D>(ln, w, tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE,
-                            pm == full_mask && rows == kKv, rows, pm, rshift, clean);
+            convert_tile<D, SCALED>(ln, w, tiles + (isv ? Ly::V_OFF : Ly::K_OFF) + st * Ly::TILE,
+                                    pm == full_mask && rows == kKv, rows, pm, rshift, clean,
+                                    isv ? scales[j & (kScaleSlots - 1)].v
+                                        : scales[j & (kScaleSlots - 1)].k);
         if (seen) misc[6] = 1;
         // (a slot is used again four tiles on, when S of the tile two on, and
         // so the softmax of this one, is long over)
@@ -712,38 +765,12 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     const int j0 = alt ? c : 0, dj = alt ? 2 : 1;
     const int fast_lo = __reduce_max_sync(0xffffffffu, rv ? lo : 0);
     const int fast_hi = __reduce_min_sync(0xffffffffu, rv ? pos + 1 : 0x7fffffff);
-    int ent_next = SCALED ? pc.entry(j0, lane) : -1;
-    float ksl = 1.f, vsl = 0.f;                       // scales of this lane's piece
-    auto load_scales = [&](int e, float& k, float& v) {
-      k = 1.f;
-      v = 0.f;
-      if (SCALED && e >= 0 && e < a.num_blocks) {
-        k = a.k_scales[(int64_t)e * a.num_kv_heads + kvh];
-        v = a.v_scales[(int64_t)e * a.num_kv_heads + kvh];
-      }
-    };
-    if (SCALED) {
-      load_scales(ent_next, ksl, vsl);
-      ent_next = pc.entry(j0 + dj, lane);
-    }
     float m_use = kNegInfC, l = 0.f, vref = 0.f;
     int t = 0;
     for (int j = j0; j < ntiles; j += dj, ++t) {
       const int ts = kv_lo + j * kKv;
       const int te = min(kv_end, ts + kKv);
-      float ks_next = 1.f, vs_next = 0.f;
-      int ent_2 = -1;
-      float alpha_v = 1.f, rcp_ref = 0.f;
-      if (SCALED) {
-        load_scales(ent_next, ks_next, vs_next);
-        ent_2 = pc.entry(j + 2 * dj, lane);
-        const float top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vsl)));
-        if (top > vref) {
-          if (vref > 0.f) alpha_v = vref / top;
-          vref = top;
-        }
-        rcp_ref = vref > 0.f ? 1.f / vref : 0.f;
-      }
+      float alpha_v = 1.f, f = f0;
       // the tile in two steps of 64 tokens
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
@@ -754,6 +781,12 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         if (!idle) {
           uint32_t v[kHalf];
           const unsigned pm = tile_mask[j & 3];
+          if (SCALED && h == 0) {
+            const TileScales& sc = scales[j & (kScaleSlots - 1)];
+            f = f0 * sc.k_ref;
+            if (vref > 0.f) alpha_v = vref / sc.v_ref;
+            vref = sc.v_ref;
+          }
           tmem_ld64(sadr + h * kHalf, v);
           const bool whole = pm == full_mask && te - ts == kKv;
           // rare paths are marked as such, which keeps the common one together
@@ -783,28 +816,14 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
             }
           }
           // pass 1: the maximum
-          float mx = kNegInfC;
-          if (!SCALED) {
-            float m4[4] = {kNegInfC, kNegInfC, kNegInfC, kNegInfC};
+          float m4[4] = {kNegInfC, kNegInfC, kNegInfC, kNegInfC};
 #pragma unroll
-            for (int e = 0; e < kHalf; e += 8)
+          for (int e = 0; e < kHalf; e += 8)
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                m4[k] = cfmax3(m4[k], __uint_as_float(v[e + 2 * k]),
-                               __uint_as_float(v[e + 2 * k + 1]));
-            mx = cfmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * f0;
-          } else {
-#pragma unroll
-            for (int g = 0; g < kHalf / 8; ++g) {
-              const float kf =
-                  __shfl_sync(0xffffffffu, ksl, (h * kHalf + 8 * g) >> rshift) * f0;
-              float m0 = fmaxf(__uint_as_float(v[8 * g]), __uint_as_float(v[8 * g + 1]));
-              float m1 = fmaxf(__uint_as_float(v[8 * g + 2]), __uint_as_float(v[8 * g + 3]));
-              m0 = cfmax3(m0, __uint_as_float(v[8 * g + 4]), __uint_as_float(v[8 * g + 5]));
-              m1 = cfmax3(m1, __uint_as_float(v[8 * g + 6]), __uint_as_float(v[8 * g + 7]));
-              mx = fmaxf(mx, fmaxf(m0, m1) * kf);
-            }
-          }
+            for (int k = 0; k < 4; ++k)
+              m4[k] = cfmax3(m4[k], __uint_as_float(v[e + 2 * k]),
+                             __uint_as_float(v[e + 2 * k + 1]));
+          const float mx = cfmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * f;
           const float m_new = fmaxf(m_use, mx);
           float alpha = 1.f;
           if (m_use == kNegInfC) {
@@ -818,19 +837,12 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
           const float nm = m_use == kNegInfC ? 0.f : -m_use;
           uint64_t sum0 = pair(0.f, 0.f), sum1 = sum0;
           const uint64_t cm = pair(nm, nm);
-          uint64_t fm = pair(f0, f0), rm = 0;
+          const uint64_t fm = pair(f, f);
 #pragma unroll
           for (int ch = 0; ch < kHalf / 32; ++ch) {
             uint32_t pk[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              if (SCALED && (e & 7) == 0) {
-                const int src = (h * kHalf + ch * 32 + e) >> rshift;
-                const float kf = __shfl_sync(0xffffffffu, ksl, src) * f0;
-                const float rt = __shfl_sync(0xffffffffu, vsl, src) * rcp_ref;
-                fm = pair(kf, kf);
-                rm = pair(rt, rt);
-              }
               float x0, x1;
               unpair(fma_pair(pair(__uint_as_float(v[ch * 32 + e]),
                                    __uint_as_float(v[ch * 32 + e + 1])), fm, cm), x0, x1);
@@ -838,7 +850,6 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
               x1 = cex2(x1);
               const uint64_t p = pair(x0, x1);
               if (e & 2) sum1 = add_pair(sum1, p); else sum0 = add_pair(sum0, p);
-              if (SCALED) unpair(mul_pair(p, rm), x0, x1);
               pk[e >> 1] = pack_half(x0, x1);
             }
             tmem_st16(sadr + h * kHalf + ch * 16, pk);
@@ -872,11 +883,6 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
         if (lane == 0) mbar_arrive(bar + 8u * (kPFull + 2 * c + h));
       }
       if (!ok) break;
-      if (SCALED) {
-        ent_next = ent_2;
-        ksl = ks_next;
-        vsl = vs_next;
-      }
     }
     if (ok) ok = mbar_wait_bounded(bar + 8u * kDone, 0, abort_flag, kWaitCycles);
     if (ok) ok = mbar_wait_bounded(bar + 8u * kConvDone, 0, abort_flag, kWaitCycles);
@@ -888,6 +894,8 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     float4* second_o =
         reinterpret_cast<float4*>(smem_raw + (tiles - sbase) + Ly::K_OFF);
     constexpr int PIECES = D / 4;
+    float* second_ml =
+        reinterpret_cast<float*>(smem_raw + (tiles - sbase) + Ly::RAW_OFF);   // [2][128]
     if (alt && c == 1) {
       if (ok && t > 0 && !idle) {
 #pragma unroll 1
