@@ -1068,6 +1068,9 @@ int run_chunk(const void* q, const int32_t* query_start_loc, int num_seqs, int64
   pa::chunk_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_seq_len,
                  window, partition_size, g_sm_count[dev], &a.rows_per_cta, &a.num_splits,
                  &a.partition);
+  a.by_length = window == 0 &&
+                pa::chunk_by_length(num_seqs, num_kv_heads, num_q_heads / num_kv_heads,
+                                    max_query_len, g_sm_count[dev], a.num_splits);
   a.ws_acc = nullptr; a.ws_ml = nullptr;
   const int64_t need = chunk_workspace(num_tokens, num_q_heads, head_size, a.num_splits);
   if (need > 0) {

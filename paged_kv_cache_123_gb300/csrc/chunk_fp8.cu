@@ -103,7 +103,7 @@ struct ChunkLayout {
   // the limit of 227 KB for head size 128
   static constexpr int BAR_OFF = 0;
   // words: 0 tmem base, 1 abort flag, 2-5 piece masks of the raw stages, 6
-  // NaN codes met, 8-11 piece masks of the last four K tiles
+  // NaN codes met, 7 the sequence, 8-11 piece masks of the last four K tiles
   static constexpr int MISC_OFF = (kBars * 8 + 15) / 16 * 16;
   static constexpr int ROW_OFF = MISC_OFF + 64;                 // float [2][128] Q row factors
   static constexpr int SCALE_OFF = ROW_OFF + 2 * kRows * 4;     // TileScales of the last tiles
@@ -255,6 +255,14 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tm, bool isv, con
     if (lane == 0 && it >= nraw)
       ok = mbar_wait_bounded(bar + 8u * (kRawEmpty + st), ((it >> raw_log2) - 1) & 1, abort_flag,
                              kWaitCycles);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (!ok) break;
+    // the copies are on their way before they are announced: the barrier's
+    // phase also needs the announcement's arrival
+    if (mine)
+      tma_load_3d(tiles + Ly::RAW_OFF + st * Ly::RAW + lane * pc.R * D, tm, 0,
+                  tok & (a.block_size - 1), (int)((int64_t)ent * a.num_kv_heads + kvh),
+                  bar + 8u * (kRawFull + st));
     if (with_scales) {
       // scales are positive: their bits order as they do
       float k_ref =
@@ -276,18 +284,10 @@ __device__ void produce(const ChunkArgs& a, const CUtensorMap* tm, bool isv, con
       __syncwarp();
     }
     if (lane == 0) {
-      if (ok) {
-        masks[st] = pm;
-        mbar_arrive_expect_tx(bar + 8u * (kRawFull + st),
-                              (uint32_t)__popc(pm) * (uint32_t)(pc.R * D));
-      }
+      masks[st] = pm;
+      mbar_arrive_expect_tx(bar + 8u * (kRawFull + st),
+                            (uint32_t)__popc(pm) * (uint32_t)(pc.R * D));
     }
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (!ok) break;
-    if (mine)
-      tma_load_3d(tiles + Ly::RAW_OFF + st * Ly::RAW + lane * pc.R * D, tm, 0,
-                  tok & (a.block_size - 1), (int)((int64_t)ent * a.num_kv_heads + kvh),
-                  bar + 8u * (kRawFull + st));
     issued = j + 1;
   }
   // this warp's copies land before the CTA can leave, also after a timeout: the
@@ -609,7 +609,26 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     return;
   }
 
-  const int s = blockIdx.z, kvh = blockIdx.y;
+  int s = blockIdx.z;
+  const int kvh = blockIdx.y;
+  if (a.by_length) {
+    // sequence number blockIdx.z in falling order of length
+    int* lens = reinterpret_cast<int*>(row_factor);
+    if (threadIdx.x < a.num_seqs) lens[threadIdx.x] = a.seq_lens[threadIdx.x];
+    __syncthreads();
+    if (threadIdx.x < a.num_seqs) {
+      const int mine = lens[threadIdx.x];
+      int rank = 0;
+#pragma unroll 8
+      for (int u = 0; u < a.num_seqs; ++u) {
+        const int len = lens[u];
+        rank += len > mine || (len == mine && u < (int)threadIdx.x);
+      }
+      if (rank == (int)blockIdx.z) misc[7] = threadIdx.x;
+    }
+    __syncthreads();
+    s = misc[7];
+  }
   const int row_tiles =
       (int)(((int64_t)a.max_query_len * G + a.rows_per_cta - 1) / a.rows_per_cta);
   const int qt = row_tiles - 1 - (int)(blockIdx.x % row_tiles);    // longest rows first
@@ -1155,6 +1174,19 @@ static int64_t span_of(int group, int max_query_len, int max_seq_len, int window
   const int64_t toks =
       std::min<int64_t>(max_query_len, rows_per_cta(group, max_query_len) / group);
   return std::min<int64_t>(len, (int64_t)window - 1 + toks + kKv - 1);
+}
+
+// Whether CTAs take the sequences in falling order of length. A ragged batch
+// in the order given leaves some SMs with a long sequence at the end: with
+// CTAs for a few waves (one to sixteen; more even out by themselves), the
+// longest first shortens that tail, for a search of some 1,000 clocks per
+// CTA.
+bool chunk_by_length(int num_seqs, int num_kv_heads, int group, int max_query_len, int sm_count,
+                     int splits) {
+  const int64_t R = rows_per_cta(group, max_query_len);
+  const int64_t ctas = ((int64_t)max_query_len * group + R - 1) / R * num_kv_heads * num_seqs;
+  return num_seqs > 1 && num_seqs <= 2 * kRows && splits == 1 && ctas > sm_count &&
+         ctas <= 16 * (int64_t)sm_count;
 }
 
 void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,

@@ -193,6 +193,7 @@ cudaError_t launch_multi_query(const MultiQueryArgs& a, cudaStream_t st);
 // span, sized from the SM count when partition_size is 0.
 struct ChunkArgs : MultiQueryArgs {
   int rows_per_cta;         // 128 or 256
+  int by_length;            // CTAs take the sequences in falling order of length
   int window;               // 0 = the whole sequence
   float k_scale, v_scale;   // one scale per pool ...
   const float* k_scales;    // ... or [num_blocks][num_kv_heads] each
@@ -201,6 +202,8 @@ struct ChunkArgs : MultiQueryArgs {
 void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,
                 int window, int partition_size, int sm_count, int* rows, int* splits,
                 int* tokens);
+bool chunk_by_length(int num_seqs, int num_kv_heads, int group, int max_query_len, int sm_count,
+                     int splits);
 cudaError_t launch_chunk_fp8(const ChunkArgs& a, cudaStream_t st);
 
 // The attention launch alone (no partition combine) of the tcgen05 kernel
