@@ -189,7 +189,8 @@ PA_API int pa_reshape_and_cache(const void* k, const void* v, int64_t num_tokens
  * A release that the ring has no room for, or an inconsistent ring state,
  * latches PA_ERR_OUT_OF_RANGE and changes nothing. A finished request whose
  * length is negative or exceeds its table row is left alone (same code).
- * One block held by two requests is a caller error.
+ * One block held by two requests is a caller error. Calls on one ring (or on
+ * the same tables) have to be ordered, as on one stream.
  *
  * Both are asynchronous and need no workspace. block_size >= 1,
  * num_tokens and ring_size below 2^31. int32 pointers must be 4-byte and
@@ -544,9 +545,12 @@ PA_API int pa_decode_attention_fp8_scaled(const void* q, const void* key_cache,
  * are exact in fp16, a bf16 query row is scaled by a power of two so that
  * its values are exact down to 2^-24 of the largest (an element below that
  * is rounded there). A masked token never reaches a row, whatever its K and
- * V hold (NaN included).
- * A V scale more than 2^24 below the largest of the sequence loses weight
- * precision, as in pa_decode_attention_fp8_scaled.
+ * V hold (NaN included). max_seq_len is below 2^31 - 1023.
+ * Per-block scales enter relative to a reference (K: the largest of 128
+ * consecutive tokens, V: the largest so far): exact for powers of two down to
+ * 2^-15 of it; a smaller one loses low bits of its codes (what is lost is
+ * below 2^-24 of the largest value under the reference), and a ratio that is
+ * no power of two is rounded to 11 bits.
  * partition_size  tokens per partition of the keys that one CTA's (token,
  *               query head) rows span, rounded up to 128; 0 picks one from
  *               the SM count. Results are reproducible bit for bit for

@@ -60,6 +60,8 @@ int elt_bytes(int dtype) {
 
 int run_rotary(pa::RotaryArgs& a, void* stream);
 
+// positions of whole 128-token tiles stay within int
+constexpr int kChunkMaxLen = 0x7fffffff - 1023;
 // partial outputs [num_tokens][Hq][splits][D], maxima and sums [..][splits][2]
 int64_t chunk_workspace(int64_t num_tokens, int num_q_heads, int head_size, int splits) {
   if (splits <= 1) return 0;
@@ -606,7 +608,8 @@ int64_t pa_multi_query_fp8_workspace_bytes(int64_t num_tokens, int num_seqs, int
   int st = check_mq_shape(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
                           max_query_len, max_seq_len);
   if (st != PA_OK) return st;
-  if (num_tokens < 0 || num_tokens > 0x7fffffffll || window < 0 || partition_size < 0)
+  if (num_tokens < 0 || num_tokens > 0x7fffffffll || window < 0 || partition_size < 0 ||
+      max_seq_len > kChunkMaxLen)
     return PA_ERR_SHAPE;
   int dev;
   st = device_setup(&dev);
@@ -1043,7 +1046,7 @@ int run_chunk(const void* q, const int32_t* query_start_loc, int num_seqs, int64
   if (st != PA_OK) return st;
   if (num_blocks < 0 || num_blocks * num_kv_heads > 0x7fffffffll || block_tables_stride < 0 ||
       num_tokens < 0 || num_tokens > 0x7fffffffll || partition_size < 0 || window < 0 ||
-      num_q_heads > 65535)
+      num_q_heads > 65535 || max_seq_len > kChunkMaxLen)
     return PA_ERR_SHAPE;
   if ((int64_t)max_seq_len > block_tables_stride * block_size) return PA_ERR_OUT_OF_RANGE;
   if (num_seqs == 0 || max_query_len == 0 || num_tokens == 0) return PA_OK;

@@ -1214,6 +1214,7 @@ void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, in
       }
     }
   }
+  P = std::min<int64_t>(P, 1 << 30);
   *rows = (int)R;
   *tokens = (int)P;
   *splits = (int)((len + P - 1) / P);

@@ -192,6 +192,44 @@ def test_partitions_meet(partition, dtype, G, n_new, pool):
 
 
 @pytest.mark.parametrize("pool", POOLS)
+def test_many_ragged_sequences(pool):
+    """Enough CTAs for several waves: sequences are taken by falling length,
+    equal lengths and empty ones among them."""
+    rng = np.random.default_rng(8)
+    ctx = rng.integers(0, 260, 100).tolist()
+    ctx[7] = ctx[8] = ctx[90]
+    new = rng.integers(1, 4, 100).tolist()
+    new[0] = new[55] = 0
+    ctx[55] = 0
+    check(make("bf16", 64, 4, 2, 16, ctx, new, pool, 91))
+
+
+@pytest.mark.parametrize("n", [31, 32, 33, 64])
+def test_rows_around_two_tiles(n):
+    """255 to 264 rows per KV head: whole pairs of row tiles and one more."""
+    check(make("f16", 128, 8, 1, 32, [0, 150, 400], [n, n, 1], "blocks", 300 + n))
+
+
+def test_block_scales_far_apart():
+    """Scales from 2^-12 to 2^12 in one sequence: what a small one loses is
+    counted with the reference, the largest scale (half of fp16's smallest
+    step, 2^-25, of each code)."""
+    c = make("bf16", 128, 8, 1, 16, [500], [40], "blocks", 92)
+    rng = np.random.default_rng(3)
+    for k in ("ks", "vs"):
+        c[k] = np.exp2(rng.integers(-12, 13, c[k].shape)).astype(np.float32)
+    c["scale"] = 2.0 ** -12 * 128 ** -0.5
+    out = call(c, on_gpu(c)).double().cpu().numpy()
+    want, tol = reference(c)
+    q = np.abs(oracle.upcast(np_(c["q"]), "bf16")).sum(-1, keepdims=True)
+    dx = c["scale"] * q * 2.0 ** -25 * c["ks"].max()
+    extra = 2 * dx * 448 * c["vs"].max() + 2.0 ** -25 * c["vs"].max()
+    assert (np.abs(out - want) <= tol + extra).all()
+    # and it is the large blocks that are right to the usual tolerance
+    assert (np.abs(out - want) <= tol + 2.0 ** -20 * np.abs(want).max()).mean() > 0.99
+
+
+@pytest.mark.parametrize("pool", POOLS)
 def test_single_tokens_split_by_themselves_and_agree_with_decode(pool):
     c = make("bf16", 128, 16, 2, 16, [10, 4999, 2000, 0], [1, 1, 1, 1], pool, 31)
     g = on_gpu(c)

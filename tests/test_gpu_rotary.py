@@ -152,6 +152,37 @@ def run_batch(counts, hkv, B, dtype, seed):
     return c
 
 
+def test_block_scales_with_many_heads_and_odd_blocks():
+    """More KV heads than a CTA's warps take at once, one-token blocks, a
+    block longer than a round of tokens, pairs next to each other."""
+    for hkv, D, B, dtype, inter in ((70, 16, 1, "bf16", False), (9, 256, 48, "f32", True),
+                                    (3, 96, 256, "f16", False)):
+        gen = torch.Generator().manual_seed(B)
+        T = 61
+        c = make(T, hkv, hkv, D, D, 2, B, dtype, 40 + B)
+        nb = -(-T // B)
+        perm = torch.randperm(nb + 2, generator=gen)
+        c["NB"] = nb + 2
+        c["slots"] = perm[:nb][torch.arange(T) // B] * B + torch.arange(T) % B
+        kc = torch.zeros(c["NB"], hkv, B, D, dtype=torch.uint8, device=DEV)
+        vc, ks = kc.clone(), torch.full((c["NB"], hkv), 3.0, device=DEV)
+        vs = ks.clone()
+        run(c, inter, kc, vc, ks, vs)
+        y, _ = formula(c["k"], c, inter)
+        v = oracle.upcast(np_(c["v"]), dtype)
+        blk = (c["slots"] // B).numpy()
+        for b in range(c["NB"]):
+            for h in range(hkv):
+                if not (blk == b).any():
+                    assert float(ks[b, h]) == 3.0
+                    continue
+                amax = np.abs(y[blk == b, h]).max()
+                near = [oracle.block_scale_e4m3(amax * f) for f in (1 - 2e-6, 1, 1 + 2e-6)]
+                assert float(ks[b, h]) in near
+                assert float(vs[b, h]) == oracle.block_scale_e4m3(np.abs(v[blk == b, h]).max())
+    assert pa.pa_get_device_error() == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("B", [4, 16, 64])
 def test_block_scales_come_from_the_rotated_values(dtype, B):

@@ -109,6 +109,7 @@ CHUNK = dict(q=P, qsl=P, S=2, T=4, kc=P, vc=P, tables=P, stride=8, lens=P, Hq=8,
     (dict(NB=1 << 31), SHAPE), (dict(NB=0), SHAPE), (dict(window=-1), SHAPE),
     (dict(max_q=-1), SHAPE), (dict(max_len=-1), SHAPE), (dict(partition=-1), SHAPE),
     (dict(k_scale=0.0), SHAPE), (dict(v_scale=float("nan")), SHAPE), (dict(max_len=129), -5),
+    (dict(max_len=0x7fffffff, stride=1 << 40), SHAPE),
     (dict(q=None), NULL), (dict(qsl=None), NULL), (dict(kc=None), NULL), (dict(vc=None), NULL),
     (dict(tables=None), NULL), (dict(lens=None), NULL), (dict(out=None), NULL),
     (dict(q=P + 8), ALIGN), (dict(kc=P + 1), ALIGN), (dict(out=P + 2), ALIGN),
