@@ -20,7 +20,7 @@
 // Small steps are therefore ONE launch of one thread-block cluster (up to 8
 // CTAs): each CTA sums its share of the requests, the totals meet through
 // distributed shared memory, and the same threads then fill the token rows.
-// Steps with more token rows than kFusedTokens run the fill on the whole GPU
+// Steps with more token rows run the fill on the whole GPU
 // in a second launch that overlaps its start with programmatic dependent
 // launch.
 #include <cooperative_groups.h>
@@ -334,29 +334,47 @@ __device__ __forceinline__ bool is_block(const ReleaseArgs& a, int32_t id) {
   return id >= 0 && id < a.num_blocks;
 }
 
-// One warp per row: the row's valid entries, counted into
-// release_start_loc[r + 1].
+// ---- rows of table entries, a warp each
+__device__ __forceinline__ int count_ids(const ReleaseArgs& a, const int32_t (&id)[kAtOnce]) {
+  int c = 0;
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) {
+    if (is_block(a, id[k])) ++c;
+    else if (id[k] >= 0) latch(a.err, PA_ERR_OUT_OF_RANGE);
+  }
+  return c;
+}
+__device__ __forceinline__ void load_ids(const int32_t* row, int64_t j0, int64_t end,
+                                         int32_t (&id)[kAtOnce]) {
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) {
+    const int64_t j = j0 + 32 * k + (threadIdx.x & 31);
+    id[k] = j < end ? row[j] : -1;
+  }
+}
+
+// Valid entries among the first `held` of a row, the first of which are in
+// id.
+__device__ __forceinline__ int count_row(const ReleaseArgs& a, const int32_t* row, int held,
+                                         const int32_t (&id)[kAtOnce]) {
+  int c = count_ids(a, id);
+  for (int j0 = 32 * kAtOnce; j0 < held; j0 += 32 * kAtOnce) {
+    int32_t more[kAtOnce];
+    load_ids(row, j0, held, more);
+    c += count_ids(a, more);
+  }
+  return __reduce_add_sync(0xffffffffu, c);
+}
+
+// Counts of the rows into release_start_loc[r + 1].
 __device__ __forceinline__ void count_rows(const ReleaseArgs& a, int first, int step) {
-  const int lane = threadIdx.x & 31;
   for (int r = first; r < a.num_seqs; r += step) {
-    const int n = held_entries(a, r);
+    const int held = held_entries(a, r);
     const int32_t* row = a.block_tables + (int64_t)r * a.table_stride;
-    int c = 0;
-    for (int j0 = 0; j0 < n; j0 += 32 * kAtOnce) {
-      int32_t id[kAtOnce];
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const int j = j0 + 32 * k + lane;
-        id[k] = j < n ? row[j] : -1;
-      }
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        if (is_block(a, id[k])) ++c;
-        else if (id[k] >= 0) latch(a.err, PA_ERR_OUT_OF_RANGE);
-      }
-    }
-    c = __reduce_add_sync(0xffffffffu, c);
-    if (lane == 0) a.release_start_loc[r + 1] = c;
+    int32_t id[kAtOnce];
+    load_ids(row, 0, held, id);
+    const int c = count_row(a, row, held, id);
+    if ((threadIdx.x & 31) == 0) a.release_start_loc[r + 1] = c;
   }
 }
 
@@ -371,7 +389,7 @@ __device__ __forceinline__ void scan_rows(const ReleaseArgs& a, Sum2* warp_sums,
   Sum2 mine{0, 0}, total;
   for (int r = lo + (int)threadIdx.x; r < hi; r += kPlanThreads)
     mine.a += a.release_start_loc[r + 1];
-  block_exclusive(mine, warp_sums, &total);
+  Sum2 ex = block_exclusive(mine, warp_sums, &total);
   const ClusterSums cs = cluster_sums(total, slot);
   const bool ok =
       ring_ok(head, tail, a.ring_size) && cs.all.a <= a.ring_size - (tail - head);
@@ -384,9 +402,12 @@ __device__ __forceinline__ void scan_rows(const ReleaseArgs& a, Sum2* warp_sums,
   int64_t carry = cs.before.a;
   for (int r0 = lo; r0 < hi; r0 += kPlanThreads) {
     const int r = r0 + (int)threadIdx.x;
-    const Sum2 v{r < hi ? a.release_start_loc[r + 1] : 0, 0};
-    __syncthreads();
-    const Sum2 ex = block_exclusive(v, warp_sums, &total);
+    Sum2 v = mine;
+    if (hi - lo > kPlanThreads) {
+      v = Sum2{r < hi ? a.release_start_loc[r + 1] : 0, 0};
+      __syncthreads();
+      ex = block_exclusive(v, warp_sums, &total);
+    }
     if (r < hi) {
       a.release_start_loc[r + 1] = ok ? (int32_t)(carry + ex.a + v.a) : 0;
       const int32_t L = a.seq_lens[r];
@@ -397,55 +418,97 @@ __device__ __forceinline__ void scan_rows(const ReleaseArgs& a, Sum2* warp_sums,
   }
 }
 
+// Ring entries of a warp's 32 x kAtOnce table entries, of which `done` valid
+// ones came before in the row; the row returns n, the first to ring entry
+// base + at.
+__device__ __forceinline__ void put_ids(const ReleaseArgs& a, const int32_t (&id)[kAtOnce],
+                                        int64_t base, int64_t at, int n, int& done) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < kAtOnce; ++k) {
+    const bool mine = is_block(a, id[k]);
+    const unsigned m = __ballot_sync(0xffffffffu, mine);
+    const int x = done + __popc(m & ((1u << lane) - 1u));
+    if (mine && x < n) a.free_ring[ring_at(base, at + x, a.ring_size)] = id[k];
+    done += __popc(m);
+  }
+}
 // One warp per row: its valid entries, in table order, to the ring behind
 // the rows before it. The row's count says how far to look, so the lengths
 // may have been cleared in place.
 __device__ __forceinline__ void return_rows(const ReleaseArgs& a, int first, int step) {
-  const int lane = threadIdx.x & 31;
   const int64_t total = a.release_start_loc[a.num_seqs];
   const int64_t tail = a.ring_state_out[1] - total;
   const int64_t base = a.ring_size > 0 ? tail % a.ring_size : 0;
   for (int r = first; r < a.num_seqs; r += step) {
     const int64_t at = a.release_start_loc[r];
     const int n = (int)(a.release_start_loc[r + 1] - at);
-    if (n > 0) {
-      const int32_t* row = a.block_tables + (int64_t)r * a.table_stride;
-      int done = 0;
-      for (int64_t j0 = 0; done < n && j0 < a.table_stride; j0 += 32 * kAtOnce) {
-        int32_t id[kAtOnce];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const int64_t j = j0 + 32 * k + lane;
-          id[k] = j < a.table_stride ? row[j] : -1;
-        }
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const bool mine = is_block(a, id[k]);
-          const unsigned m = __ballot_sync(0xffffffffu, mine);
-          const int x = done + __popc(m & ((1u << lane) - 1u));
-          if (mine && x < n) a.free_ring[ring_at(base, at + x, a.ring_size)] = id[k];
-          done += __popc(m);
-        }
-      }
+    const int32_t* row = a.block_tables + (int64_t)r * a.table_stride;
+    int done = 0;
+    for (int64_t j0 = 0; done < n && j0 < a.table_stride; j0 += 32 * kAtOnce) {
+      int32_t id[kAtOnce];
+      load_ids(row, j0, a.table_stride, id);
+      put_ids(a, id, base, at, n, done);
     }
   }
 }
 
+// The whole release in one cluster, a warp per row: the rows' counts meet
+// through distributed shared memory, every CTA sums all of them, and the
+// entries that were counted (the first 512 of a row, from registers) go to
+// the ring.
 __global__ void __launch_bounds__(kPlanThreads) release_one_kernel(const ReleaseArgs a) {
   __shared__ Sum2 warp_sums[kPlanWarps];
-  __shared__ Sum2 slot;
+  __shared__ int counts[kPlanWarps];
+  __shared__ int starts[kPlanMaxCluster * kPlanWarps];
   cg::cluster_group cl = cg::this_cluster();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = (int)cl.block_rank() * kPlanWarps + warp;
   griddep_launch();
   griddep_wait();
-  const int w = (int)cl.block_rank() * kPlanWarps + (int)(threadIdx.x >> 5);
-  const int nw = (int)cl.num_blocks() * kPlanWarps;
-  count_rows(a, w, nw);
-  __threadfence();
+  const int64_t head = a.ring_state[0], tail = a.ring_state[1];
+  const bool row_is = r < a.num_seqs;
+  const int L = row_is ? a.seq_lens[r] : 0;
+  const int held = row_is ? held_entries(a, r) : 0;
+  const int32_t* row = a.block_tables + (int64_t)r * a.table_stride;
+  int32_t id[kAtOnce];
+  load_ids(row, 0, held, id);
+  const int n = count_row(a, row, held, id);
+  if (lane == 0) counts[warp] = n;
   cl.sync();
-  scan_rows(a, warp_sums, &slot);
-  __threadfence();
-  cl.sync();
-  return_rows(a, w, nw);
+  const int other = (int)threadIdx.x / kPlanWarps;
+  const Sum2 v{other < (int)cl.num_blocks() ? cl.map_shared_rank(counts, other)[lane] : 0, 0};
+  Sum2 total;
+  const Sum2 ex = block_exclusive(v, warp_sums, &total);
+  if (threadIdx.x < kPlanMaxCluster * kPlanWarps) starts[threadIdx.x] = (int)min(ex.a, (int64_t)0x7fffffff);
+  __syncthreads();
+  const bool ok =
+      ring_ok(head, tail, a.ring_size) && total.a <= a.ring_size - (tail - head);
+  if (r == 0 && lane == 0) {
+    if (!ok) latch(a.err, PA_ERR_OUT_OF_RANGE);
+    a.release_start_loc[0] = 0;
+    // every CTA has read the state (cluster barrier above)
+    a.ring_state_out[0] = head;
+    a.ring_state_out[1] = ok ? tail + total.a : tail;
+  }
+  if (row_is) {
+    const int at = starts[r];
+    if (lane == 0) {
+      a.release_start_loc[r + 1] = ok ? at + n : 0;
+      const bool gone = ok && a.finished[r] != 0 && L >= 0 && L <= a.table_stride * a.block_size;
+      a.seq_lens_out[r] = gone ? 0 : L;
+    }
+    if (ok && n > 0) {
+      const int64_t base = tail % a.ring_size;
+      int done = 0;
+      put_ids(a, id, base, at, n, done);
+      for (int64_t j0 = 32 * kAtOnce; done < n && j0 < held; j0 += 32 * kAtOnce) {
+        load_ids(row, j0, held, id);
+        put_ids(a, id, base, at, n, done);
+      }
+    }
+  }
+  cl.sync();            // no CTA leaves while another reads its counts
 }
 
 __global__ void __launch_bounds__(256) release_count_kernel(const ReleaseArgs a) {
@@ -496,14 +559,21 @@ int cluster_for(int64_t threads) {
   return ctas <= 1 ? 1 : ctas <= 2 ? 2 : ctas <= 4 ? 4 : kPlanMaxCluster;
 }
 
-// token rows that the cluster itself fills; table entries that it returns
-constexpr int64_t kFusedTokens = 4 * kPlanMaxCluster * kPlanThreads;
-constexpr int64_t kFusedEntries = 256 * 1024;
+// Token rows that the cluster itself fills: the second launch costs some 2
+// us (5 to 7 with many requests, whose sums and table writes it repeats), the
+// fill on eight SMs 0.2 us per 1,024 rows. One launch against two: 64
+// requests, 16,384 rows 7.9 and 8.9 us, 32,768 rows 10.2 and 9.0; 8,192
+// requests, 32,768 rows 15.3 and 18.4, 65,536 rows 21.8 and 18.1.
+int64_t fused_tokens(int num_seqs) { return 24 * 1024 + 2 * (int64_t)num_seqs; }
+// Requests that one cluster releases, a warp each; three launches take, in
+// one launch's place, 7.6 us instead of 5.4 (128 requests of up to 4k tokens
+// in blocks of 16), 13.8 instead of 11.8 (256 of up to 32k).
+constexpr int kFusedRows = kPlanMaxCluster * kPlanWarps;
 
 }  // namespace
 
 cudaError_t launch_extend_tables(const ExtendArgs& a, int sm_count, cudaStream_t st) {
-  if (a.num_tokens <= kFusedTokens)
+  if (a.num_tokens <= fused_tokens(a.num_seqs))
     return launch_cluster(extend_plan_kernel<true>,
                           cluster_for(a.num_tokens > a.num_seqs ? a.num_tokens : a.num_seqs),
                           staged_bytes(a.num_seqs), st, a);
@@ -519,7 +589,7 @@ cudaError_t launch_extend_tables(const ExtendArgs& a, int sm_count, cudaStream_t
 }
 
 cudaError_t launch_release_tables(const ReleaseArgs& a, int sm_count, cudaStream_t st) {
-  if ((int64_t)a.num_seqs * a.table_stride <= kFusedEntries)
+  if (a.num_seqs <= kFusedRows)
     return launch_cluster(release_one_kernel, cluster_for((int64_t)a.num_seqs * 32), 0, st, a);
   const int threads = 256, rows = threads / 32;
   int64_t blocks = ((int64_t)a.num_seqs + rows - 1) / rows;
