@@ -614,9 +614,9 @@ int64_t pa_multi_query_fp8_workspace_bytes(int64_t num_tokens, int num_seqs, int
   int dev;
   st = device_setup(&dev);
   if (st != PA_OK) return st;
-  int rows, splits, tokens;
+  int splits, tokens;
   pa::chunk_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_seq_len,
-                 window, partition_size, g_sm_count[dev], &rows, &splits, &tokens);
+                 window, partition_size, g_sm_count[dev], &splits, &tokens);
   return chunk_workspace(num_tokens, num_q_heads, head_size, splits);
 }
 
@@ -1069,11 +1069,10 @@ int run_chunk(const void* q, const int32_t* query_start_loc, int num_seqs, int64
   a.window = window; a.k_scale = k_scale; a.v_scale = v_scale;
   a.k_scales = k_scales; a.v_scales = v_scales;
   pa::chunk_plan(num_seqs, num_kv_heads, num_q_heads / num_kv_heads, max_query_len, max_seq_len,
-                 window, partition_size, g_sm_count[dev], &a.rows_per_cta, &a.num_splits,
-                 &a.partition);
+                 window, partition_size, g_sm_count[dev], &a.num_splits, &a.partition);
   a.by_length = window == 0 &&
                 pa::chunk_by_length(num_seqs, num_kv_heads, num_q_heads / num_kv_heads,
-                                    max_query_len, g_sm_count[dev], a.num_splits);
+                                    max_query_len, max_seq_len, g_sm_count[dev], a.num_splits);
   a.ws_acc = nullptr; a.ws_ml = nullptr;
   const int64_t need = chunk_workspace(num_tokens, num_q_heads, head_size, a.num_splits);
   if (need > 0) {

@@ -64,6 +64,11 @@ namespace pa {
 namespace {
 
 constexpr int kRows = 128;                // rows of a chain (MMA M)
+// Rows of a CTA. Two row tiles share each key tile's widening; with CTAs of
+// one tile 8 x 512 tokens after 4k take 1,036 us instead of 529, and one
+// chunk of 32 tokens x 8 heads after 2k, with twice the CTAs for its two
+// tiles, 27.7 instead of 26.6.
+constexpr int kCtaRows = 2 * kRows;
 constexpr int kKv = 128;                  // KV tokens per tile
 constexpr int kMmaWarp = 0;
 constexpr int kProducerWarp = 1;          // K, and 2: V
@@ -96,6 +101,7 @@ struct TileScales {
   float k_ref, v_ref, unused[2];
 };
 constexpr int kScaleSlots = 8;
+constexpr int kMaxOrdered = kThreads / 4;  // sequences taken by length at most
 
 template <int D>
 struct ChunkLayout {
@@ -171,6 +177,10 @@ __device__ __forceinline__ uint32_t pack_out<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+__host__ __device__ inline int64_t row_tiles_of(int max_query_len, int group) {
+  return ((int64_t)max_query_len * group + kCtaRows - 1) / kCtaRows;
+}
+
 // What a row tile covers: tokens i_first .. i_last of the sequence's new
 // ones, keys kv_base (a multiple of the tile) .. kv_all - 1, of which those
 // before kv_first are in no row's window; `count` partitions.
@@ -179,14 +189,14 @@ struct TileSpan {
 };
 __device__ __forceinline__ TileSpan tile_span(const ChunkArgs& a, int G, int n, int L, int qt) {
   TileSpan t;
-  const int r0 = qt * a.rows_per_cta;
+  const int r0 = qt * kCtaRows;
   t.i_first = r0 / G;
-  t.i_last = min(n - 1, (r0 + a.rows_per_cta - 1) / G);
+  t.i_last = min(n - 1, (r0 + kCtaRows - 1) / G);
   t.kv_all = L - n + t.i_last + 1;
   const int p0 = L - n + t.i_first;
   t.kv_first = a.window > 0 && p0 + 1 > a.window ? p0 + 1 - a.window : 0;
   t.kv_base = t.kv_first & ~(kKv - 1);
-  t.count = (t.kv_all - t.kv_base + a.partition - 1) / a.partition;
+  t.count = (t.kv_all - t.kv_base - 1) / a.partition + 1;
   return t;
 }
 __device__ __forceinline__ bool lengths_ok(const ChunkArgs& a, int q0, int n, int L) {
@@ -613,24 +623,34 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
   const int kvh = blockIdx.y;
   if (a.by_length) {
     // sequence number blockIdx.z in falling order of length
-    int* lens = reinterpret_cast<int*>(row_factor);
-    if (threadIdx.x < a.num_seqs) lens[threadIdx.x] = a.seq_lens[threadIdx.x];
-    __syncthreads();
-    if (threadIdx.x < a.num_seqs) {
-      const int mine = lens[threadIdx.x];
-      int rank = 0;
-#pragma unroll 8
-      for (int u = 0; u < a.num_seqs; ++u) {
-        const int len = lens[u];
-        rank += len > mine || (len == mine && u < (int)threadIdx.x);
-      }
-      if (rank == (int)blockIdx.z) misc[7] = threadIdx.x;
+    uint32_t* keys = reinterpret_cast<uint32_t*>(row_factor);
+    // the length's 24 leading bits (of those max_seq_len has) and the index:
+    // no two alike, and the words behind the last sequence outrank none
+    const int drop = max(0, 8 - __clz(a.max_seq_len));
+    if (threadIdx.x < kMaxOrdered) {
+      uint32_t key = 0;
+      if (threadIdx.x < a.num_seqs)
+        key = (uint32_t)(min(max(a.seq_lens[threadIdx.x], 0), a.max_seq_len) >> drop) << 8 |
+              (kMaxOrdered - 1 - threadIdx.x);
+      keys[threadIdx.x] = key;
     }
+    __syncthreads();
+    // a sequence's place is the number of larger keys, counted by four threads
+    const int u = threadIdx.x >> 2;
+    const uint32_t mine = keys[u];
+    int rank = 0;
+#pragma unroll 4
+    for (int x = threadIdx.x & 3; 4 * x < a.num_seqs; x += 4) {
+      const uint4 k = reinterpret_cast<const uint4*>(keys)[x];
+      rank += (k.x > mine) + (k.y > mine) + (k.z > mine) + (k.w > mine);
+    }
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (u < a.num_seqs && rank == (int)blockIdx.z) misc[7] = u;
     __syncthreads();
     s = misc[7];
   }
-  const int row_tiles =
-      (int)(((int64_t)a.max_query_len * G + a.rows_per_cta - 1) / a.rows_per_cta);
+  const int row_tiles = (int)row_tiles_of(a.max_query_len, G);
   const int qt = row_tiles - 1 - (int)(blockIdx.x % row_tiles);    // longest rows first
   const int split = (int)(blockIdx.x / row_tiles);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -641,12 +661,12 @@ chunk_fp8_kernel(const ChunkArgs a, const __grid_constant__ CUtensorMap tmK,
     if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) latch(a.err, PA_ERR_OUT_OF_RANGE);
     return;
   }
-  const int r0 = qt * a.rows_per_cta;
+  const int r0 = qt * kCtaRows;
   if (r0 >= n * G) return;
   const TileSpan sp = tile_span(a, G, n, L, qt);
-  const int kv_lo = sp.kv_base + split * a.partition;
   if (split >= sp.count) return;
-  const int kv_end = min(sp.kv_all, kv_lo + a.partition);
+  const int kv_lo = sp.kv_base + split * a.partition;
+  const int kv_end = kv_lo + min(sp.kv_all - kv_lo, a.partition);
   const int ntiles = (kv_end - kv_lo + kKv - 1) / kKv;
   const bool alt = n * G - r0 <= kRows;             // one row tile: key tiles in turn
   const int raw_log2 = alt ? 2 : 1, nraw = 1 << raw_log2;
@@ -1061,7 +1081,7 @@ __global__ void __launch_bounds__(D) chunk_combine_kernel(const ChunkArgs a) {
   if (s < 0 || s >= a.num_seqs) return;
   const int q0 = a.qsl[s], n = a.qsl[s + 1] - q0, L = a.seq_lens[s];
   if (!lengths_ok(a, q0, n, L)) return;
-  const TileSpan sp = tile_span(a, G, n, L, (int)(((t - q0) * G + head % G) / a.rows_per_cta));
+  const TileSpan sp = tile_span(a, G, n, L, (int)(((t - q0) * G + head % G) / kCtaRows));
   if (sp.count <= 1) return;
   const int64_t base = (t * a.num_q_heads + head) * a.num_splits;
   float M = kNegInfC;
@@ -1124,8 +1144,7 @@ cudaError_t launch_chunk(const ChunkArgs& a, cudaStream_t st) {
                                 cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::SMEM);
   });
   if (attr != cudaSuccess) return attr;
-  const int64_t row_tiles =
-      ((int64_t)a.max_query_len * G + a.rows_per_cta - 1) / a.rows_per_cta;
+  const int64_t row_tiles = row_tiles_of(a.max_query_len, G);
   if (row_tiles * a.num_splits > 0x7fffffffll) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)(row_tiles * a.num_splits), a.num_kv_heads, a.num_seqs);
   chunk_fp8_kernel<T, D, G, SCALED><<<grid, kThreads, Ly::SMEM, st>>>(a, tk, tv);
@@ -1162,46 +1181,48 @@ cudaError_t launch_chunk_d(const ChunkArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Rows of a CTA: one tile where no sequence has more, two otherwise.
-static int64_t rows_per_cta(int group, int max_query_len) {
-  return (int64_t)max_query_len * group > kRows ? 2 * kRows : kRows;
-}
-
 // Keys a CTA's rows can span (the kernel's tile_span).
 static int64_t span_of(int group, int max_query_len, int max_seq_len, int window) {
   const int64_t len = max_seq_len > 0 ? max_seq_len : 1;
   if (window <= 0) return len;
   const int64_t toks =
-      std::min<int64_t>(max_query_len, rows_per_cta(group, max_query_len) / group);
+      std::min<int64_t>(max_query_len, kCtaRows / group);
   return std::min<int64_t>(len, (int64_t)window - 1 + toks + kKv - 1);
 }
 
 // Whether CTAs take the sequences in falling order of length. A ragged batch
-// in the order given leaves some SMs with a long sequence at the end: with
-// CTAs for a few waves (one to sixteen; more even out by themselves), the
-// longest first shortens that tail, for a search of some 1,000 clocks per
-// CTA.
-bool chunk_by_length(int num_seqs, int num_kv_heads, int group, int max_query_len, int sm_count,
-                     int splits) {
-  const int64_t R = rows_per_cta(group, max_query_len);
-  const int64_t ctas = ((int64_t)max_query_len * group + R - 1) / R * num_kv_heads * num_seqs;
-  return num_seqs > 1 && num_seqs <= 2 * kRows && splits == 1 && ctas > sm_count &&
-         ctas <= 16 * (int64_t)sm_count;
+// in the order given leaves some SMs with a long sequence at the end; with
+// CTAs for one to sixteen waves (more even out by themselves) the longest
+// first shortens that tail, for a search of some 1,000 clocks per CTA, which
+// short sequences would feel. In the order given and by length: 128 sequences
+// of 1k to 8k tokens 385 and 362 us, 32 chunks of 128 after 0 to 4k 312 and
+// 294; all of 4k 315 and 320; 128 of 100 to 400 tokens 75.6 and 78.8.
+bool chunk_by_length(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,
+                     int sm_count, int splits) {
+  const int64_t ctas = row_tiles_of(max_query_len, group) * num_kv_heads * num_seqs;
+  return num_seqs > 1 && num_seqs <= kMaxOrdered && max_seq_len >= 2048 && splits == 1 &&
+         ctas > sm_count && ctas <= 16 * (int64_t)sm_count;
 }
 
+// Partitions of the keys, where the CTAs alone would leave SMs idle: the
+// number that minimises the waves' keys, with 256 tokens' time for the start
+// of a CTA and again for the merge. With a wave of CTAs or more there is
+// little to gain, and the parts of ragged sequences cannot be taken longest
+// first; unsplit against split (4 tokens a sequence, 8 KV heads): 32
+// sequences of 1k to 8k tokens 98 and 134 us, 64 of them 182 and 225, 36 of
+// 6k 129 and 129, 24 of 6k 127 and 112. Below a wave: 12 of 1k to 8k 83 and
+// 69, 8 of 4k 47 and 32, one of 8k 82 and 17.
 void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,
-                int window, int partition_size, int sm_count, int* rows, int* splits,
-                int* tokens) {
+                int window, int partition_size, int sm_count, int* splits, int* tokens) {
   const int64_t len = span_of(group, max_query_len, max_seq_len, window);
   auto round_up = [](int64_t x) { return (x + kKv - 1) / kKv * kKv; };
   int64_t P = round_up(len);
-  const int64_t R = rows_per_cta(group, max_query_len);
   if (partition_size > 0) {
     P = std::min(P, round_up(partition_size));
   } else {
-    const int64_t row_tiles = ((int64_t)max_query_len * group + R - 1) / R;
-    const int64_t ctas = std::max<int64_t>(1, row_tiles * num_kv_heads * num_seqs);
-    if (ctas < 4 * (int64_t)sm_count) {
+    const int64_t ctas = std::max<int64_t>(
+        1, row_tiles_of(max_query_len, group) * num_kv_heads * num_seqs);
+    if (ctas < (int64_t)sm_count) {
       int64_t best = -1;
       for (int64_t k = 1; k <= 64 && (k == 1 || len / k >= 256); ++k) {
         const int64_t p = round_up((len + k - 1) / k);
@@ -1215,7 +1236,6 @@ void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, in
     }
   }
   P = std::min<int64_t>(P, 1 << 30);
-  *rows = (int)R;
   *tokens = (int)P;
   *splits = (int)((len + P - 1) / P);
 }

@@ -189,10 +189,9 @@ struct MultiQueryArgs {
 cudaError_t launch_multi_query(const MultiQueryArgs& a, cudaStream_t st);
 
 // The same over fp8 (E4M3) pools, with a sliding window (chunk_fp8.cu).
-// chunk_plan: rows of a CTA, and the partitions of the keys that they can
-// span, sized from the SM count when partition_size is 0.
+// chunk_plan: partitions of the keys that a CTA's rows can span, sized from
+// the SM count when partition_size is 0.
 struct ChunkArgs : MultiQueryArgs {
-  int rows_per_cta;         // 128 or 256
   int by_length;            // CTAs take the sequences in falling order of length
   int window;               // 0 = the whole sequence
   float k_scale, v_scale;   // one scale per pool ...
@@ -200,10 +199,9 @@ struct ChunkArgs : MultiQueryArgs {
   const float* v_scales;
 };
 void chunk_plan(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,
-                int window, int partition_size, int sm_count, int* rows, int* splits,
-                int* tokens);
-bool chunk_by_length(int num_seqs, int num_kv_heads, int group, int max_query_len, int sm_count,
-                     int splits);
+                int window, int partition_size, int sm_count, int* splits, int* tokens);
+bool chunk_by_length(int num_seqs, int num_kv_heads, int group, int max_query_len, int max_seq_len,
+                     int sm_count, int splits);
 cudaError_t launch_chunk_fp8(const ChunkArgs& a, cudaStream_t st);
 
 // The attention launch alone (no partition combine) of the tcgen05 kernel

@@ -331,13 +331,16 @@ cudaError_t launch_rotary_t(const RotaryArgs& a, int sm_count, cudaStream_t st) 
   }
   // few tokens: one per CTA, so that they spread over the SMs; more: two or
   // four per CTA, which share a round's barriers, as long as that leaves
-  // several waves of CTAs (some five are resident per SM)
+  // several waves of CTAs (some five are resident per SM). With 1, 2 and 4
+  // tokens per CTA (64 + 2 x 8 heads of 128, bf16): 608 tokens 7.0, 9.3, 8.2
+  // us; 1,216 tokens 11.8, 10.9, 16.0; 2,432 tokens 23.2, 20.3, 20.2; 4,864 tokens 44.6, 40.4, 38.4; 36,000
+  // tokens 289, 249, 237.
   auto go = [&](auto kernel, int tok) {
     const int64_t blocks = std::min<int64_t>((a.num_tokens + tok - 1) / tok, 0x7fffffffll);
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRotThreads), 0, st, a);
   };
-  if (a.num_tokens <= (int64_t)sm_count * 8) return go(rotary_kernel<T, POOL, INTER, 1>, 1);
-  if (a.num_tokens <= (int64_t)sm_count * 80) return go(rotary_kernel<T, POOL, INTER, 2>, 2);
+  if (a.num_tokens <= (int64_t)sm_count * 5) return go(rotary_kernel<T, POOL, INTER, 1>, 1);
+  if (a.num_tokens <= (int64_t)sm_count * 30) return go(rotary_kernel<T, POOL, INTER, 2>, 2);
   return go(rotary_kernel<T, POOL, INTER, 4>, 4);
 }
 

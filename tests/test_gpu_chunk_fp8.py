@@ -204,6 +204,41 @@ def test_many_ragged_sequences(pool):
     check(make("bf16", 64, 4, 2, 16, ctx, new, pool, 91))
 
 
+@pytest.mark.parametrize("pool", POOLS)
+@pytest.mark.parametrize("S", [77, 80, 128, 129])
+def test_long_sequences_are_taken_first(S, pool):
+    """Up to 128 sequences with more CTAs than SMs and lengths past 2,048 are
+    taken by falling length: equal lengths and empty sequences among them, the
+    longest ones last in the batch."""
+    rng = np.random.default_rng(S)
+    ctx = rng.integers(0, 300, S).tolist()
+    ctx[-1], ctx[-2], ctx[5] = 2101, 2101, 2200
+    ctx[9] = ctx[10] = ctx[60]
+    new = rng.integers(1, 4, S).tolist()
+    new[0] = new[55] = 0
+    ctx[55] = 0
+    check(make("bf16", 64, 8, 4, 16, ctx, new, pool, 93))
+
+
+def test_positions_next_to_the_largest_length():
+    """A window at the end of 2^31 - 1,024 tokens, whose earlier blocks are
+    released; one partition and several."""
+    B, D, w, n, L = 256, 64, 300, 5, 0x7fffffff - 1023
+    c = make("bf16", D, 2, 1, B, [600], [n], "blocks", 94, window=w)
+    g = on_gpu(c)
+    near = c["lens"][0]
+    shift = (L - int(near)) // B * B              # the same place in its block
+    want = reference(c)
+    cols = (int(near) + shift + B - 1) // B
+    t = torch.full((1, cols), -1, dtype=torch.int32, device=DEV)
+    t[0, shift // B:] = g["tables"][0, :cols - shift // B]
+    g["tables"] = t
+    g["lens"] = g["lens"] + shift
+    for part in (0, 128):
+        close(call(c, g, max_seq_len=L - L % B, partition_size=part), want)
+    assert pa.pa_get_device_error() == 0
+
+
 @pytest.mark.parametrize("n", [31, 32, 33, 64])
 def test_rows_around_two_tiles(n):
     """255 to 264 rows per KV head: whole pairs of row tiles and one more."""
