@@ -78,7 +78,7 @@ def same(got, want):
 
 
 # one CTA, a whole cluster, several tiles per CTA, and the two-launch form
-# (more than 32,768 token rows)
+# (more token rows than 24,576 and two per request)
 SHAPES = [(1, 16, 0, 1), (2, 1, 5, 3), (3, 3, 40, 9), (127, 16, 500, 1), (1024, 8, 30, 2),
           (1025, 16, 100, 40), (5000, 256, 700, 5), (8192, 16, 40, 3), (20000, 4, 9, 1),
           (9000, 16, 20, 30), (64, 128, 2000, 900), (1, 16, 7, 50000)]
@@ -285,6 +285,42 @@ def test_release_matches_the_sequential_rule(S, B, ctx_hi, holes):
     assert np.array_equal(g["tables"].cpu().numpy(), c["tables"])
     again = release(c, g, torch.tensor(fin, device=DEV))     # their length is 0: nothing twice
     assert not again["rsl"].any() and again["state"].tolist() == want["state"].tolist()
+    assert pa.pa_get_device_error() == 0
+
+
+@pytest.mark.parametrize("S", [1, 31, 32, 33, 255, 256, 257])
+def test_release_of_long_rows_around_a_cluster(S):
+    """Rows of more than 512 and 1,024 entries, entries of other pools and
+    released ones among them; one launch up to 256 requests."""
+    c = make(S, 4, 5000, 0, 7 * S, head=11)
+    rng = np.random.default_rng(S + 1)
+    c["ctx"][S // 2] = 4 * 1200 if c["tables"].shape[1] >= 1200 else c["ctx"][S // 2]
+    c["tables"][rng.random(c["tables"].shape) < 0.2] = -1
+    fin = np.ones(S, bool)
+    fin[1::5] = False
+    g = gpu(c)
+    want = ref_release(fin, c["ctx"], c["tables"], 4, c["ring"], c["head"], c["tail"], c["NB"])
+    same(release(c, g, torch.tensor(fin, device=DEV)), want)
+    assert pa.pa_get_device_error() == 0
+    # the same into other arrays: lengths and state are kept
+    g = gpu(c)
+    out = dict(seq_lens_out=torch.empty(S, dtype=torch.int32, device=DEV),
+               ring_state_out=torch.empty(2, dtype=torch.int64, device=DEV))
+    same(release(c, g, torch.tensor(fin, device=DEV), **out), want)
+    assert np.array_equal(g["ctx"].cpu().numpy(), c["ctx"])
+    assert g["state"].tolist() == [c["head"], c["tail"]]
+
+
+@pytest.mark.parametrize("S", [3, 900])
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_extend_around_the_rows_of_one_launch(S, more):
+    c = make(S, 16, 500, 24 * 1024 // S, S + more + 5)
+    rows = 24 * 1024 + 2 * S + more
+    assert c["T"] <= rows
+    c["T"] = rows
+    g = gpu(c)
+    same(extend(c, g), ref_extend(c["ctx"], c["new"], c["tables"], 16, c["ring"], c["head"],
+                                  c["tail"], rows))
     assert pa.pa_get_device_error() == 0
 
 
