@@ -182,12 +182,13 @@ __device__ __forceinline__ int64_t slot_of(const ExtendArgs& a, const RowPlace& 
   return (int64_t)blk * a.block_size + w.row;
 }
 
-// Token rows: warp `first` of `step` takes `groups` x 64 consecutive rows at a
-// time, a lane two of each 64. The requests of the warp's first and last row
+// Token rows: warp `first` of `step` takes `groups` x 32 ROWS consecutive rows
+// at a time, a lane ROWS (1 or 2) of each group. The requests of the warp's first and last row
 // are searched once (every lane the same loads); a lane then searches between
 // them, which for prompts is next to no search. Rows behind the last token are
 // padding (position 0, slot -1). `qsl` is query_start_loc or a copy in shared
 // memory, `head` the ring head before this step.
+template <int ROWS>
 __device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* qsl, int64_t head,
                                             int64_t first, int64_t step, int groups) {
   const int lane = threadIdx.x & 31;
@@ -196,7 +197,7 @@ __device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* 
   const int shift = (a.block_size & (a.block_size - 1)) == 0 ? __ffs(a.block_size) - 1 : -1;
   const bool pairs = (reinterpret_cast<uintptr_t>(a.positions) & 15) == 0 &&
                      (reinterpret_cast<uintptr_t>(a.slot_mapping) & 15) == 0;
-  const int64_t span = 64 * (int64_t)groups;
+  const int64_t span = 32 * ROWS * (int64_t)groups;
   for (int64_t t0 = first * span; t0 < a.num_tokens; t0 += step * span) {
     int lo = 0, hi = a.num_seqs;
     if (t0 < total) {
@@ -205,13 +206,13 @@ __device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* 
     }
 #pragma unroll 2
     for (int g = 0; g < groups; ++g) {
-      const int64_t t = t0 + 64 * g + 2 * lane;
+      const int64_t t = t0 + 32 * ROWS * g + ROWS * lane;
       longlong2 pos = make_longlong2(0, 0), slot = make_longlong2(-1, -1);
       if (t < total) {
         // both rows' loads before either's stores
         const int r = request_of(qsl, t, lo, hi);
         const RowPlace w0 = place_row(a, qsl, r, t, base, shift);
-        const bool two = t + 1 < total;
+        const bool two = ROWS == 2 && t + 1 < total;
         RowPlace w1 = w0;
         if (two)
           w1 = place_row(a, qsl, (int64_t)qsl[r + 1] <= t + 1 ? request_of(qsl, t + 1, r, hi) : r,
@@ -224,12 +225,12 @@ __device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* 
           slot.y = slot_of(a, w1, b1);
         }
       }
-      if (pairs && t + 1 < a.num_tokens) {
+      if (ROWS == 2 && pairs && t + 1 < a.num_tokens) {
         *reinterpret_cast<longlong2*>(a.positions + t) = pos;
         *reinterpret_cast<longlong2*>(a.slot_mapping + t) = slot;
       } else {
         if (t < a.num_tokens) { a.positions[t] = pos.x; a.slot_mapping[t] = slot.x; }
-        if (t + 1 < a.num_tokens) { a.positions[t + 1] = pos.y; a.slot_mapping[t + 1] = slot.y; }
+        if (ROWS == 2 && t + 1 < a.num_tokens) { a.positions[t + 1] = pos.y; a.slot_mapping[t + 1] = slot.y; }
       }
     }
   }
@@ -246,7 +247,8 @@ __device__ __forceinline__ const int32_t* stage_starts(const ExtendArgs& a, int3
 }
 int staged_bytes(int num_seqs) { return num_seqs > kStagedSeqs ? 0 : (num_seqs + 1) * 4; }
 
-template <bool FUSED>
+// ROWS: token rows of a lane at a time in the same launch, 0: in the next one.
+template <int ROWS>
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendArgs a) {
   extern __shared__ int32_t staged[];
   __shared__ Sum2 warp_sums[kPlanWarps];
@@ -303,10 +305,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const ExtendA
     carry.a += total.a;
     carry.b += total.b;
   }
-  if (FUSED) __threadfence();
-  cl.sync();            // shared memory of this CTA is no longer read; FUSED: sums visible
-  if (FUSED)
-    fill_tokens(a, stage_starts(a, staged), head,
+  if (ROWS > 0) __threadfence();
+  cl.sync();            // shared memory of this CTA is no longer read; ROWS: sums visible
+  if (ROWS > 0)
+    fill_tokens<ROWS>(a, stage_starts(a, staged), head,
                 (int64_t)rank * kPlanWarps + (threadIdx.x >> 5), (int64_t)count * kPlanWarps, 1);
 }
 
@@ -315,8 +317,9 @@ __global__ void __launch_bounds__(kFillThreads) extend_fill_kernel(const ExtendA
   griddep_launch();
   griddep_wait();
   const int64_t head = a.ring_state_out[0] - a.block_start_loc[a.num_seqs];
-  fill_tokens(a, stage_starts(a, staged), head, (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5),
-              (int64_t)gridDim.x * (blockDim.x >> 5), kFillGroups);
+  fill_tokens<2>(a, stage_starts(a, staged), head,
+                 (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5),
+                 (int64_t)gridDim.x * (blockDim.x >> 5), kFillGroups);
 }
 
 // Table entries that request r holds, 0 if it is not finished; a length
@@ -574,12 +577,16 @@ constexpr int kFusedRows = kPlanMaxCluster * kPlanWarps;
 }  // namespace
 
 cudaError_t launch_extend_tables(const ExtendArgs& a, int sm_count, cudaStream_t st) {
+  // a row per thread while the cluster has one for each: the chain is shorter
+  // than with two (128 requests, 128 rows 6.2 and 6.8 us; 64 requests, 4,096
+  // rows 6.6 and 7.0, 16,384 rows 8.8 and 7.6)
   if (a.num_tokens <= fused_tokens(a.num_seqs))
-    return launch_cluster(extend_plan_kernel<true>,
+    return launch_cluster(a.num_tokens <= kPlanMaxCluster * kPlanThreads ? extend_plan_kernel<1>
+                                                                         : extend_plan_kernel<2>,
                           cluster_for(a.num_tokens > a.num_seqs ? a.num_tokens : a.num_seqs),
                           staged_bytes(a.num_seqs), st, a);
   cudaError_t e =
-      launch_cluster(extend_plan_kernel<false>, cluster_for(a.num_seqs), 0, st, a);
+      launch_cluster(extend_plan_kernel<0>, cluster_for(a.num_seqs), 0, st, a);
   if (e != cudaSuccess) return e;
   // two CTAs per SM at most: each stages the start rows once
   const int rows = kFillThreads / 32 * 64 * kFillGroups;
