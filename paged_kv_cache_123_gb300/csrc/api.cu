@@ -1044,7 +1044,7 @@ int run_chunk(const void* q, const int32_t* query_start_loc, int num_seqs, int64
   int st = check_mq_shape(num_seqs, num_q_heads, num_kv_heads, head_size, block_size,
                           max_query_len, max_seq_len);
   if (st != PA_OK) return st;
-  if (num_blocks < 0 || num_blocks * num_kv_heads > 0x7fffffffll || block_tables_stride < 0 ||
+  if (num_blocks < 0 || num_blocks > 0x7fffffffll / num_kv_heads || block_tables_stride < 0 ||
       num_tokens < 0 || num_tokens > 0x7fffffffll || partition_size < 0 || window < 0 ||
       num_q_heads > 65535 || max_seq_len > kChunkMaxLen)
     return PA_ERR_SHAPE;

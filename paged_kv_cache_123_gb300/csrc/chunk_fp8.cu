@@ -32,6 +32,29 @@
 //   * a softmax thread owns one row: scores in registers, running maximum
 //     and sum in fp32; the output in TMEM is rescaled only when the maximum
 //     grew by more than 2^8.
+// The steps are halves of a key tile, which makes four streams of scores
+// (all in flight: a stream's next scores are issued one step late, behind the
+// next stream's P V). A key tile takes 256 rows some 3,700 clocks, of which
+// the MMAs need 2,590 by their measured rates (64 clocks for 128 x 128 x 16,
+// 49 for the scores' 128 x 64 x 16); what is left is each stream's chain of
+// scores, maximum, exponentials, P, P V and next scores, which four streams
+// do not quite cover.
+//
+// Replayed from a graph (64 query and 8 KV heads of 128, bf16, blocks of 16,
+// one scale): 8 x 512 tokens after 4k 523 us, 1,116 TFLOP/s, 0.58 of the
+// measured bf16 rate; 4 tokens x 128 sequences of 1k
+// to 8k 357 us, 3.5 TB/s of codes, 0.52 of the copy rate: a 32-row tile costs
+// the softmax and the MMAs as much as a full one. 4 x 256 tokens (32 heads,
+// fp16) over 32k with scales per block 598 us, 924 TFLOP/s; 16 ragged chunks
+// of up to 511 with a window of 1,000 208 us: with ten key tiles per CTA its
+// start (some 10,000 clocks: Q) and end (4,000) are a quarter.
+// Measured and dropped: whole-row softmax steps of 128 keys with larger
+// register shares (669 us for the 8 x 512 case, then at 609), one step that
+// finds the maximum and redoes the exponentials where it grew (540 against
+// 533), eight converter warps (536 against 526), an MMA warp that takes
+// whichever stream is ready (636 against 531), waits by one lane (749 against
+// 609).
+//
 // fp16 products for both query types: weights are rounded to 11 bits, one
 // rounding, in [0, 2^8].
 //
