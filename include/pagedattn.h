@@ -226,7 +226,8 @@ PA_API int pa_release_block_tables(const uint8_t* finished, const int32_t* seq_l
  *                elements apart; k, v likewise with num_kv_heads: slices of
  *                one fused projection need no copy.
  *   q_out        rows of [num_q_heads][head_size], q_out_stride elements
- *                apart; every row is written. May be q with the same stride.
+ *                apart; every row is written. May be q with the same stride;
+ *                must not overlap k, v or the pools.
  *   positions    int64 [num_axes], rows of num_tokens, position_stride apart.
  *   inv_freq     float64 [rot_size / 2], device.
  *   axis_of_pair int32 [rot_size / 2], device, entries in [0, num_axes)

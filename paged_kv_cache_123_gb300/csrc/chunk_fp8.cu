@@ -63,8 +63,9 @@
 // the logit factor, for V the largest so far, which the output is in units of
 // (it is rescaled when that reference grows). Powers of two keep this exact
 // down to 2^-15 of the reference; below, low bits go as they would with one
-// scale equal to the reference. (Factors on the scores and weights in the
-// softmax warps, where shuffles fetched them, cost 25 % of the kernel.)
+// scale equal to the reference. (With the factors on the scores and
+// weights in the softmax warps 4 x 256 tokens over 32k took 660 us instead of
+// 611.)
 //
 // NaN codes: a masked weight is 0, but 0 x NaN is NaN inside the MMA, so a
 // NaN in V could reach rows that do not see its token. Tiles that some row

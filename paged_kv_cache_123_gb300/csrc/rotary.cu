@@ -24,8 +24,8 @@
 // Replayed from a graph, 64 query and 8 KV heads of 128, bf16, three axes:
 // 32,500 tokens into 16-bit pools 215 us (1.33 GB: 6.2 TB/s, 0.91 of the
 // measured copy rate); 4,400 tokens into blocks with scales 43.5 us (171 MB,
-// 25 us at the copy rate; the scales' pass reads k and v a second time and
-// ends 5 us or so before the rows it serves); 64 tokens of 32 + 2 x 32 heads,
+// 25 us at the copy rate; k and v are read twice and wait for the scales; 47.6
+// when q waited too); 64 tokens of 32 + 2 x 32 heads,
 // fp16, 3.9 us (3.1 MB: the launch). The angle work is what kept it from the
 // copy rate: with FP64 frequencies and range reduction the blocks' case took
 // 105 us. A persistent grid measured 318 us for the first case, and a table
