@@ -23,10 +23,10 @@
 //
 // Replayed from a graph, 64 query and 8 KV heads of 128, bf16, three axes:
 // 32,500 tokens into 16-bit pools 215 us (1.33 GB: 6.2 TB/s, 0.91 of the
-// measured copy rate); 4,400 tokens into blocks with scales 43.5 us (171 MB,
-// 25 us at the copy rate; k and v are read twice and wait for the scales; 47.6
-// when q waited too); 64 tokens of 32 + 2 x 32 heads,
-// fp16, 3.9 us (3.1 MB: the launch). The angle work is what kept it from the
+// measured copy rate); 4,400 tokens into blocks with scales 47.6 us (171 MB,
+// 25 us at the copy rate; everything waits for the scales' pass, which reads k
+// and v once more); 64 tokens of 32 + 2 x 32 heads, fp16, 3.9 us (3.1 MB: the
+// launch). The angle work is what kept it from the
 // copy rate: with FP64 frequencies and range reduction the blocks' case took
 // 105 us. A persistent grid measured 318 us for the first case, and a table
 // of turns in shared memory 240: short CTAs hide one another's start better.
@@ -120,10 +120,6 @@ __device__ __forceinline__ void store_fp8(uint8_t* dst, const float* f, float sc
 // or the neighbours at 2c*N and 2c*N + N (interleaved), later units the
 // neighbours at 2c*N (dims that pass).
 // POOL: 0 pools of T, 1 E4M3 with one scale, 2 E4M3 with per-block scales.
-// With per-block scales the q rows are turned while the scales are found by
-// the launch before: that one lets this kernel start only once its own CTAs
-// have waited for the work before them, so q is there; k and v wait for its
-// end.
 template <typename T, int POOL, bool INTER, int TOK>
 __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a) {
   constexpr int N = Vec<T>::N;
@@ -143,7 +139,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
   const int e1 = rot && !INTER ? half + c * N : e0 + N;       // second vector's
   const int heads = a.num_q_heads + 2 * a.num_kv_heads;
   const int64_t limit = a.num_blocks * a.block_size;
-  if (POOL != 2) griddep_wait();
+  griddep_wait();
   for (int64_t t0 = (int64_t)blockIdx.x * TOK; t0 < a.num_tokens;
        t0 += (int64_t)gridDim.x * TOK) {
     const int nt = (int)min((int64_t)TOK, a.num_tokens - t0);
@@ -164,69 +160,55 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
       slot_of[threadIdx.x] = s < limit ? s : -1;
     }
     __syncthreads();
-    if (!active) {
-      if (POOL == 2) griddep_wait();
-      continue;
-    }
-    // heads first .. first + count - 1 of the round's tokens
-    auto run = [&](int first, int count) {
-      int tk = 0, x = lane_row;
-      while (true) {
-        while (x >= count) { x -= count; ++tk; }
-        if (tk >= nt) break;
-        const int h = first + x;
-        const int64_t t = t0 + tk;
-        const int64_t slot = slot_of[tk];
-        const int kind = h < a.num_q_heads ? 0 : h < a.num_q_heads + a.num_kv_heads ? 1 : 2;
-        const int kvh = h - a.num_q_heads - (kind == 2 ? a.num_kv_heads : 0);
-        if (kind == 0 || slot >= 0) {
-          const T* src = kind == 0 ? (const T*)a.q + t * a.q_stride + (int64_t)h * D
-                       : kind == 1 ? (const T*)a.k + t * a.k_stride + (int64_t)kvh * D
-                                   : (const T*)a.v + t * a.v_stride + (int64_t)kvh * D;
-          const uint4 u0 = *reinterpret_cast<const uint4*>(src + e0);
-          const uint4 u1 = *reinterpret_cast<const uint4*>(src + e1);
-          float x[2 * N];
-          Vec<T>::to_f32(u0, x);
-          Vec<T>::to_f32(u1, x + N);
-          if (rot && kind != 2) {
+    if (!active) continue;
+    int tk = 0, h = lane_row;
+    while (true) {
+      while (h >= heads) { h -= heads; ++tk; }
+      if (tk >= nt) break;
+      const int64_t t = t0 + tk;
+      const int64_t slot = slot_of[tk];
+      const int kind = h < a.num_q_heads ? 0 : h < a.num_q_heads + a.num_kv_heads ? 1 : 2;
+      const int kvh = h - a.num_q_heads - (kind == 2 ? a.num_kv_heads : 0);
+      if (kind == 0 || slot >= 0) {
+        const T* src = kind == 0 ? (const T*)a.q + t * a.q_stride + (int64_t)h * D
+                     : kind == 1 ? (const T*)a.k + t * a.k_stride + (int64_t)kvh * D
+                                 : (const T*)a.v + t * a.v_stride + (int64_t)kvh * D;
+        const uint4 u0 = *reinterpret_cast<const uint4*>(src + e0);
+        const uint4 u1 = *reinterpret_cast<const uint4*>(src + e1);
+        float x[2 * N];
+        Vec<T>::to_f32(u0, x);
+        Vec<T>::to_f32(u1, x + N);
+        if (rot && kind != 2) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const float2 w = cs[tk][c * N + i];
-              if (INTER) rotate(x[2 * i], x[2 * i + 1], w, x[2 * i], x[2 * i + 1]);
-              else rotate(x[i], x[N + i], w, x[i], x[N + i]);
-            }
-          }
-          if (kind == 0) {
-            T* dst = (T*)a.q_out + t * a.q_out_stride + (int64_t)h * D;
-            *reinterpret_cast<uint4*>(dst + e0) = pack16<T>(x);
-            *reinterpret_cast<uint4*>(dst + e1) = pack16<T>(x + N);
-          } else {
-            const int64_t blk = slot / a.block_size;
-            const int64_t dst =
-                ((blk * a.num_kv_heads + kvh) * a.block_size + (slot - blk * a.block_size)) * D;
-            if (POOL != 0) {
-              const float sc =
-                  POOL == 2 ? (kind == 1 ? a.k_scales : a.v_scales)[blk * a.num_kv_heads + kvh]
-                            : (kind == 1 ? a.k_scale : a.v_scale);
-              uint8_t* cache = (uint8_t*)(kind == 1 ? a.kc : a.vc) + dst;
-              store_fp8<N, POOL == 2>(cache + e0, x, sc);
-              store_fp8<N, POOL == 2>(cache + e1, x + N, sc);
-            } else {
-              T* cache = (T*)(kind == 1 ? a.kc : a.vc) + dst;
-              *reinterpret_cast<uint4*>(cache + e0) = pack16<T>(x);
-              *reinterpret_cast<uint4*>(cache + e1) = pack16<T>(x + N);
-            }
+          for (int i = 0; i < N; ++i) {
+            const float2 w = cs[tk][c * N + i];
+            if (INTER) rotate(x[2 * i], x[2 * i + 1], w, x[2 * i], x[2 * i + 1]);
+            else rotate(x[i], x[N + i], w, x[i], x[N + i]);
           }
         }
-        x += rows_at_once;
+        if (kind == 0) {
+          T* dst = (T*)a.q_out + t * a.q_out_stride + (int64_t)h * D;
+          *reinterpret_cast<uint4*>(dst + e0) = pack16<T>(x);
+          *reinterpret_cast<uint4*>(dst + e1) = pack16<T>(x + N);
+        } else {
+          const int64_t blk = slot / a.block_size;
+          const int64_t dst =
+              ((blk * a.num_kv_heads + kvh) * a.block_size + (slot - blk * a.block_size)) * D;
+          if (POOL != 0) {
+            const float sc =
+                POOL == 2 ? (kind == 1 ? a.k_scales : a.v_scales)[blk * a.num_kv_heads + kvh]
+                          : (kind == 1 ? a.k_scale : a.v_scale);
+            uint8_t* cache = (uint8_t*)(kind == 1 ? a.kc : a.vc) + dst;
+            store_fp8<N, POOL == 2>(cache + e0, x, sc);
+            store_fp8<N, POOL == 2>(cache + e1, x + N, sc);
+          } else {
+            T* cache = (T*)(kind == 1 ? a.kc : a.vc) + dst;
+            *reinterpret_cast<uint4*>(cache + e0) = pack16<T>(x);
+            *reinterpret_cast<uint4*>(cache + e1) = pack16<T>(x + N);
+          }
+        }
       }
-    };
-    if (POOL == 2) {
-      run(0, a.num_q_heads);
-      griddep_wait();
-      run(a.num_q_heads, heads - a.num_q_heads);
-    } else {
-      run(0, heads);
+      h += rows_at_once;
     }
   }
 }
@@ -253,8 +235,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_scales_kernel(const Rotary
   __shared__ int axis[kRotMaxHalf];
   __shared__ int64_t first_slot[kScaleTokens];
   __shared__ int run_len;
+  griddep_launch();
   griddep_wait();
-  griddep_launch();             // after the wait: see rotary_kernel
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int half = a.rot_size / 2, D = a.head_size, B = a.block_size;
   const int units = D / (2 * N), rot_units = a.rot_size / (2 * N);
@@ -361,8 +343,8 @@ cudaError_t launch_rotary_t(const RotaryArgs& a, int sm_count, cudaStream_t st) 
   // four per CTA, which share a round's barriers, as long as that leaves
   // several waves of CTAs (some five are resident per SM). With 1, 2 and 4
   // tokens per CTA (64 + 2 x 8 heads of 128, bf16): 608 tokens 7.0, 9.3, 8.2
-  // us; 1,216 tokens 11.8, 10.9, 16.0; 2,432 tokens 23.2, 20.3, 20.2; 4,864
-  // tokens 44.6, 40.4, 38.4; 36,000 tokens 289, 249, 237.
+  // us; 1,216 tokens 11.8, 10.9, 16.0; 2,432 tokens 23.2, 20.3, 20.2; 4,864 tokens 44.6, 40.4, 38.4; 36,000
+  // tokens 289, 249, 237.
   auto go = [&](auto kernel, int tok) {
     const int64_t blocks = std::min<int64_t>((a.num_tokens + tok - 1) / tok, 0x7fffffffll);
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRotThreads), 0, st, a);

@@ -251,7 +251,6 @@ __device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* 
 // dependent loads.
 __device__ __forceinline__ const int32_t* stage_starts(const ExtendArgs& a, int32_t* staged) {
   if (a.num_seqs > kStagedSeqs) return a.query_start_loc;
-#pragma unroll 8
   for (int i = threadIdx.x; i <= a.num_seqs; i += blockDim.x) staged[i] = a.query_start_loc[i];
   __syncthreads();
   return staged;
