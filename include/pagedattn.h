@@ -20,7 +20,8 @@
  *     stream). Every call is asynchronous on that stream; a return of PA_OK
  *     means the arguments were valid and the kernels were launched.
  *   - The decode step's kernels (slot mapping, KV writes, decode attention
- *     and its combine or merge) are launched with programmatic dependent
+ *     and its combine or merge) and those of the table and rotary calls are
+ *     launched with programmatic dependent
  *     launch: a kernel's blocks may be scheduled while the kernel before it
  *     in the stream drains, but each waits for that kernel to complete, and
  *     for its writes to be visible, before it touches memory that kernel
