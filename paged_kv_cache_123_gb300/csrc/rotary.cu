@@ -218,10 +218,10 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryArgs a)
 // row 0 of its block, the largest magnitude over the run of tokens that this
 // call puts into the block, of the ROTATED keys and of the values, fixes the
 // block's scales. A CTA looks at kScaleTokens tokens and takes the runs that
-// begin there (one, with blocks of 16) one after the other: the run's cosines and sines go to shared
-// memory, kRunTokens tokens at a time, and each warp takes KV heads, in the
-// units of rotary_kernel (the same arithmetic, so the maximum is of exactly
-// the values that the second pass quantises).
+// begin there (one, with blocks of 16) one after the other: the run's cosines
+// and sines go to shared memory, kRunTokens tokens at a time, and each warp
+// takes KV heads, in the units of rotary_kernel (the same arithmetic, so the
+// maximum is of exactly the values that the second pass quantises).
 constexpr int kScaleTokens = 16;
 constexpr int kRunTokens = 16;
 constexpr int kHeadsPerWarp = 8;
@@ -343,8 +343,8 @@ cudaError_t launch_rotary_t(const RotaryArgs& a, int sm_count, cudaStream_t st) 
   // four per CTA, which share a round's barriers, as long as that leaves
   // several waves of CTAs (some five are resident per SM). With 1, 2 and 4
   // tokens per CTA (64 + 2 x 8 heads of 128, bf16): 608 tokens 7.0, 9.3, 8.2
-  // us; 1,216 tokens 11.8, 10.9, 16.0; 2,432 tokens 23.2, 20.3, 20.2; 4,864 tokens 44.6, 40.4, 38.4; 36,000
-  // tokens 289, 249, 237.
+  // us; 1,216 tokens 11.8, 10.9, 16.0; 2,432 tokens 23.2, 20.3, 20.2; 4,864
+  // tokens 44.6, 40.4, 38.4; 36,000 tokens 289, 249, 237.
   auto go = [&](auto kernel, int tok) {
     const int64_t blocks = std::min<int64_t>((a.num_tokens + tok - 1) / tok, 0x7fffffffll);
     return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kRotThreads), 0, st, a);

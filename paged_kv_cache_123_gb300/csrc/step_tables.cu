@@ -50,8 +50,9 @@ constexpr int kFillGroups = 4;    // 64-row groups a warp takes at a time
 // takes 5.6, 5.3 and 8.3 us, the large one 25.1, 25.3 and 27.7.
 constexpr int kAtOnce = 16;
 // Requests whose query_start_loc is staged in shared memory for the searches:
-// the 48 KB that a launch has without asking for more.
-constexpr int kStagedSeqs = 12 * 1024 - 1;
+// the 48 KB that a launch has without asking for more, less 1 KB for the
+// kernels' own.
+constexpr int kStagedSeqs = 12 * 1024 - 256 - 1;
 
 struct Sum2 {
   int64_t a, b;
@@ -241,7 +242,10 @@ __device__ __forceinline__ void fill_tokens(const ExtendArgs& a, const int32_t* 
         *reinterpret_cast<longlong2*>(a.slot_mapping + t) = slot;
       } else {
         if (t < a.num_tokens) { a.positions[t] = pos.x; a.slot_mapping[t] = slot.x; }
-        if (ROWS == 2 && t + 1 < a.num_tokens) { a.positions[t + 1] = pos.y; a.slot_mapping[t + 1] = slot.y; }
+        if (ROWS == 2 && t + 1 < a.num_tokens) {
+          a.positions[t + 1] = pos.y;
+          a.slot_mapping[t + 1] = slot.y;
+        }
       }
     }
   }
@@ -255,6 +259,7 @@ __device__ __forceinline__ const int32_t* stage_starts(const ExtendArgs& a, int3
   __syncthreads();
   return staged;
 }
+static_assert((kStagedSeqs + 1) * 4 + 1024 <= 48 * 1024, "staged rows and the kernels' own");
 int staged_bytes(int num_seqs) { return num_seqs > kStagedSeqs ? 0 : (num_seqs + 1) * 4; }
 
 // ROWS: token rows of a lane at a time in the same launch, 0: in the next one.
@@ -494,7 +499,8 @@ __global__ void __launch_bounds__(kPlanThreads) release_one_kernel(const Release
   const Sum2 v{other < (int)cl.num_blocks() ? cl.map_shared_rank(counts, other)[lane] : 0, 0};
   Sum2 total;
   const Sum2 ex = block_exclusive(v, warp_sums, &total);
-  if (threadIdx.x < kPlanMaxCluster * kPlanWarps) starts[threadIdx.x] = (int)min(ex.a, (int64_t)0x7fffffff);
+  if (threadIdx.x < kPlanMaxCluster * kPlanWarps)
+    starts[threadIdx.x] = (int)min(ex.a, (int64_t)0x7fffffff);
   __syncthreads();
   const bool ok =
       ring_ok(head, tail, a.ring_size) && total.a <= a.ring_size - (tail - head);

@@ -311,6 +311,17 @@ def test_release_of_long_rows_around_a_cluster(S):
     assert g["state"].tolist() == [c["head"], c["tail"]]
 
 
+@pytest.mark.parametrize("S", [12031, 12032, 12155, 12156, 12287, 12288])
+@pytest.mark.parametrize("new", [1, 5])
+def test_extend_around_the_shared_memory_of_a_launch(S, new):
+    """Where query_start_loc stops fitting beside the kernels' own shared
+    memory, in one launch and in two."""
+    c = make(S, 16, 50, new, S + new, new_lo=new)
+    same(extend(c, gpu(c)), ref_extend(c["ctx"], c["new"], c["tables"], 16, c["ring"], c["head"],
+                                       c["tail"], c["T"]))
+    assert pa.pa_get_device_error() == 0
+
+
 @pytest.mark.parametrize("S", [3, 900])
 @pytest.mark.parametrize("more", [-1, 0, 1])
 def test_extend_around_the_rows_of_one_launch(S, more):
